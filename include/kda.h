@@ -322,6 +322,154 @@ kda_status_t kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, 
                                    int dk, int dv, int chunk_size, kda_dtype_t dtype,
                                    cudaStream_t stream);
 
+/*
+ * The operators around the recurrence in a layer: the short convolution that
+ * makes its q, k, v projections, the norm before the projections and on its
+ * output, and the selective scan, the diagonal sibling of the recurrence.
+ * (Library plumbing: the pages describe the recurrence only.)
+ *
+ * Shared by the entry points below:
+ *   - dtype is the type of the activations (bf16 or fp32).  weight_dtype is the
+ *     type of weight and bias, bf16 or fp32 on its own.  All arithmetic, sums
+ *     and states of the scan are fp32; every output is rounded once.
+ *   - Pointers need element alignment, unless stated (fp32 states of the scan:
+ *     16 bytes).  Rows that are 16-byte aligned take wider loads; others give
+ *     the same result.
+ *   - *_stride arguments are the elements from one row (token) of an input to
+ *     the next, so that a slice of a joint projection can be given as it is.
+ *     Everything else is densely packed.
+ *   - Tokens are B rows of T, or, with cu_seqlens (see kda_chunk_fwd), num_seqs
+ *     packed sequences over T tokens with B == 1; N = B or num_seqs.  A
+ *     malformed table raises the device error word (kda_device_error reports
+ *     KDA_ERR_INVALID_ARG); no read or write leaves the buffers' bounds, and
+ *     the outputs are then unspecified.  Sequences may be empty.
+ *   - Outputs must not alias inputs unless stated.  Results do not depend on
+ *     scheduling: no floating-point atomics.
+ */
+
+/*
+ * Root-mean-square norm of rows [rows, D], 1 <= D <= 16384, with the
+ * residual's addition:
+ *   s = x (+ residual);  y = s / sqrt(mean(s^2) + eps) * weight
+ *   x : dtype, x_stride >= D between rows;  residual : [rows, D] dtype or NULL
+ *   weight : [D] weight_dtype
+ *   y : [rows, D] dtype, written (may be x when x is packed)
+ *   s : [rows, D] dtype, written, or NULL (may be residual): the residual
+ *       stream, rounded; the norm is taken of the unrounded sum.
+ */
+kda_status_t kda_rms_norm_fwd(const void* x, long long x_stride, const void* residual, const void* weight,
+                              kda_dtype_t weight_dtype, void* y, void* s, long long rows, int D, float eps,
+                              kda_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * The same with an e4m3 output and fp32 scales, for an 8-bit projection:
+ *   scale = max(amax |y|, 1e-10) / 448 over each group of columns,
+ *   q = e4m3(y / scale), rounded to nearest even.
+ *   group : columns a scale; 0 (the whole row) or 32, 64, 128 dividing D.
+ *           Groups need 16-byte aligned x, residual and rows of x
+ *           (KDA_ERR_ALIGNMENT otherwise), an 8-byte aligned q, s and weight as x.
+ *   q : [rows, D] bytes;  scale : [rows, D / group] fp32 ([rows, 1] for 0)
+ * A row with a NaN gets NaN scales.
+ */
+kda_status_t kda_rms_norm_quant_fwd(const void* x, long long x_stride, const void* residual, const void* weight,
+                                    kda_dtype_t weight_dtype, void* q, float* scale, void* s, long long rows, int D,
+                                    int group, float eps, kda_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Backward of kda_rms_norm_fwd: with r = 1 / sqrt(mean(s^2) + eps),
+ *   dx = r weight dy - s r^3 mean(weight dy s) + ds   (also the residual's gradient)
+ *   dweight = sum over rows of dy s r
+ *   dy, s : [rows, D] dtype (s as the forward wrote it; x without a residual)
+ *   ds : [rows, D] dtype or NULL, the gradient that reaches s on the residual stream
+ *   dx : [rows, D] dtype (may be dy or ds);  dweight : [D] fp32
+ */
+size_t kda_rms_norm_bwd_workspace_size(long long rows, int D);
+kda_status_t kda_rms_norm_bwd(const void* dy, const void* s, const void* weight, kda_dtype_t weight_dtype,
+                              const void* ds, void* dx, float* dweight, long long rows, int D, float eps,
+                              kda_dtype_t dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Short causal depthwise convolution with SiLU, width W in {2, 3, 4}:
+ *   p_t = bias + sum_j weight[:, j] x_{t-W+1+j};  y_t = p_t sigmoid(p_t)
+ *   x : [B, T, D] dtype, x_stride >= D between tokens
+ *   weight : [D, W], bias : [D] or NULL, weight_dtype
+ *   state : [N, W-1, D] dtype or NULL (zeros): the inputs before each sequence's
+ *       first token, oldest first
+ *   y : [B, T, D] dtype;  state_out : [N, W-1, D] dtype or NULL: the last W-1
+ *       rows of (state, x) of each sequence.  Must not be state.
+ */
+kda_status_t kda_short_conv_fwd(const void* x, long long x_stride, const void* weight, const void* bias,
+                                kda_dtype_t weight_dtype, const void* state, void* y, void* state_out,
+                                const int32_t* cu_seqlens, int num_seqs, int B, int T, int D, int W,
+                                kda_dtype_t dtype, cudaStream_t stream);
+/* One token of each of N sequences: x, y [N, D]; state and state_out [N, W-1, D],
+ * state_out may be state (updated in place). */
+kda_status_t kda_short_conv_step(const void* x, long long x_stride, const void* weight, const void* bias,
+                                 kda_dtype_t weight_dtype, const void* state, void* y, void* state_out, int N, int D,
+                                 int W, kda_dtype_t dtype, cudaStream_t stream);
+/*
+ * Backward of kda_short_conv_fwd.
+ *   dy : [B, T, D] in dy_dtype (dtype or fp32: the recurrence's gradients are fp32)
+ *   dstate : [N, W-1, D] fp32 or NULL, the gradient of state_out
+ *   dx : [B, T, D] dtype;  dweight : [D, W] fp32;  dbias : [D] fp32 or NULL
+ *   dinit : [N, W-1, D] fp32 or NULL, the gradient of state
+ */
+size_t kda_short_conv_bwd_workspace_size(int B, int T, int D, int W);
+kda_status_t kda_short_conv_bwd(const void* x, long long x_stride, const void* weight, const void* bias,
+                                kda_dtype_t weight_dtype, const void* state, const void* dy, kda_dtype_t dy_dtype,
+                                const float* dstate, void* dx, float* dweight, float* dbias, float* dinit,
+                                const int32_t* cu_seqlens, int num_seqs, int B, int T, int D, int W,
+                                kda_dtype_t dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Selective state space scan: per channel a state of S numbers that decays and
+ * is written and read through vectors shared by the channels of a group,
+ *   delta_t = softplus(dt_t + dt_bias)
+ *   h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t
+ *   y_t = (C_t . h_t + Dskip x_t) z_t sigmoid(z_t)      (without z: no gate)
+ *   x, dt, z : [B, T, d] dtype, a stride each; z may be NULL
+ *   Bm, Cm : [B, T, groups, S] dtype, a stride each; channel c reads group
+ *       c / (d / groups)
+ *   A : [d, S] fp32 (negative for a decaying state);  Dskip, dt_bias : [d] fp32 or NULL
+ *   S0 : [N, d, S] fp32 or NULL (zeros);  S_out : [N, d, S] fp32 or NULL, not S0
+ *   S in {8, 16, 32, 64}; groups divides d.  A, S0, S_out and the workspace
+ *       are 16-byte aligned.
+ * Batches with few channels and packed sequences are cut into chunks of the
+ * token axis that run in parallel (up to rounding the result is the same); the
+ * workspace holds one state per chunk.
+ */
+size_t kda_selective_scan_fwd_workspace_size(int B, int T, int d, int S, int groups, int num_seqs);
+kda_status_t kda_selective_scan_fwd(const void* x, long long x_stride, const void* dt, long long dt_stride,
+                                    const float* A, const void* Bm, long long B_stride, const void* Cm,
+                                    long long C_stride, const float* Dskip, const void* z, long long z_stride,
+                                    const float* dt_bias, const float* S0, void* y, float* S_out,
+                                    const int32_t* cu_seqlens, int num_seqs, int B, int T, int d, int S, int groups,
+                                    kda_dtype_t dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* One token of each of N sequences: x, dt, z, y [N, d], Bm, Cm [N, groups, S];
+ * the state St is read and S_out written, which may be St (in place). */
+kda_status_t kda_selective_scan_step(const void* x, long long x_stride, const void* dt, long long dt_stride,
+                                     const float* A, const void* Bm, long long B_stride, const void* Cm,
+                                     long long C_stride, const float* Dskip, const void* z, long long z_stride,
+                                     const float* dt_bias, const float* St, void* y, float* S_out, int N, int d,
+                                     int S, int groups, kda_dtype_t dtype, cudaStream_t stream);
+/*
+ * Backward of kda_selective_scan_fwd, given dy : [B, T, d] dtype and, or NULL,
+ * dS : [N, d, S] fp32 (gradient of S_out).  Written:
+ *   dx, ddt, dz : [B, T, d] dtype (dz only and always with z)
+ *   dA : [d, S], dDskip, ddt_bias : [d] (either may be NULL),
+ *   dB, dC : [B, T, groups, S], dS0 : [N, d, S] or NULL, all fp32
+ *   dS, dS0 are 16-byte aligned too.
+ */
+size_t kda_selective_scan_bwd_workspace_size(int B, int T, int d, int S, int groups);
+kda_status_t kda_selective_scan_bwd(const void* x, long long x_stride, const void* dt, long long dt_stride,
+                                    const float* A, const void* Bm, long long B_stride, const void* Cm,
+                                    long long C_stride, const float* Dskip, const void* z, long long z_stride,
+                                    const float* dt_bias, const float* S0, const void* dy, const float* dS, void* dx,
+                                    void* ddt, float* dA, float* dB, float* dC, float* dDskip, void* dz,
+                                    float* ddt_bias, float* dS0, const int32_t* cu_seqlens, int num_seqs, int B,
+                                    int T, int d, int S, int groups, kda_dtype_t dtype, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
 /* Message describing the calling thread's last failure ("" if none). */
 const char* kda_last_error(void);
 

@@ -13,6 +13,12 @@ recurrent_step(q, k, v, g, beta, S, o=None)
     one decode token per sequence, S updated in place -> o
 chunk_fwd_host(...)
     chunk_fwd for pinned host tensors: copies in, runs, copies results out
+rms_norm_fwd, rms_norm_quant_fwd, rms_norm_bwd
+    root-mean-square norm with the residual's addition, e4m3 output, backward
+short_conv_fwd, short_conv_step, short_conv_bwd
+    short causal depthwise convolution with SiLU
+selective_scan_fwd, selective_scan_step, selective_scan_bwd
+    selective state space scan
 workspace_size(...), last_error(), device_error(), lib_path()
 """
 from __future__ import annotations
@@ -41,7 +47,11 @@ EXPORTED = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_recurrent_step
             "kda_set_segment_chunks", "kda_segment_chunks", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size",
             "kda_set_local_kernel", "kda_chunk_fwd_host", "kda_chunk_fwd_host_buffer_size",
             "kda_set_prefill_path", "kda_chunk_fwd_phases", "kda_gdn_chunk_bwd", "kda_chunk_bwd_prep",
-            "kda_chunk_bwd_prep_workspace_size")
+            "kda_chunk_bwd_prep_workspace_size",
+            "kda_rms_norm_fwd", "kda_rms_norm_quant_fwd", "kda_rms_norm_bwd", "kda_rms_norm_bwd_workspace_size",
+            "kda_short_conv_fwd", "kda_short_conv_step", "kda_short_conv_bwd", "kda_short_conv_bwd_workspace_size",
+            "kda_selective_scan_fwd", "kda_selective_scan_fwd_workspace_size", "kda_selective_scan_step",
+            "kda_selective_scan_bwd", "kda_selective_scan_bwd_workspace_size")
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 # Kernels of one kda_chunk_fwd call, in launch order, per path.
@@ -128,6 +138,34 @@ def load_library():
         lib.kda_chunk_fwd_phases.restype = i32
         lib.kda_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, vp]
         lib.kda_selftest_bounded_wait.restype = i32
+        i64, f32 = ctypes.c_longlong, ctypes.c_float
+        lib.kda_rms_norm_fwd.argtypes = [vp, i64, vp, vp, i32, vp, vp, i64, i32, f32, i32, vp]
+        lib.kda_rms_norm_fwd.restype = i32
+        lib.kda_rms_norm_quant_fwd.argtypes = [vp, i64, vp, vp, i32, vp, vp, vp, i64, i32, i32, f32, i32, vp]
+        lib.kda_rms_norm_quant_fwd.restype = i32
+        lib.kda_rms_norm_bwd_workspace_size.argtypes = [i64, i32]
+        lib.kda_rms_norm_bwd_workspace_size.restype = szt
+        lib.kda_rms_norm_bwd.argtypes = [vp, vp, vp, i32, vp, vp, vp, i64, i32, f32, i32, vp, szt, vp]
+        lib.kda_rms_norm_bwd.restype = i32
+        lib.kda_short_conv_fwd.argtypes = [vp, i64, vp, vp, i32, vp, vp, vp, vp] + [i32] * 6 + [vp]
+        lib.kda_short_conv_fwd.restype = i32
+        lib.kda_short_conv_step.argtypes = [vp, i64, vp, vp, i32, vp, vp, vp] + [i32] * 4 + [vp]
+        lib.kda_short_conv_step.restype = i32
+        lib.kda_short_conv_bwd_workspace_size.argtypes = [i32] * 4
+        lib.kda_short_conv_bwd_workspace_size.restype = szt
+        lib.kda_short_conv_bwd.argtypes = [vp, i64, vp, vp, i32, vp, vp, i32] + [vp] * 6 + [i32] * 6 + [vp, szt, vp]
+        lib.kda_short_conv_bwd.restype = i32
+        scan_in = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp]
+        lib.kda_selective_scan_fwd_workspace_size.argtypes = [i32] * 6
+        lib.kda_selective_scan_fwd_workspace_size.restype = szt
+        lib.kda_selective_scan_fwd.argtypes = scan_in + [vp] * 3 + [i32] * 7 + [vp, szt, vp]
+        lib.kda_selective_scan_fwd.restype = i32
+        lib.kda_selective_scan_step.argtypes = scan_in + [vp] * 2 + [i32] * 5 + [vp]
+        lib.kda_selective_scan_step.restype = i32
+        lib.kda_selective_scan_bwd_workspace_size.argtypes = [i32] * 5
+        lib.kda_selective_scan_bwd_workspace_size.restype = szt
+        lib.kda_selective_scan_bwd.argtypes = scan_in + [vp] * 12 + [i32] * 7 + [vp, szt, vp]
+        lib.kda_selective_scan_bwd.restype = i32
         lib.kda_version.argtypes = []
         lib.kda_version.restype = i32
         _lib = lib
@@ -633,6 +671,367 @@ def algorithmic_bytes_per_launch(kernel, token_heads, units, d=128, with_state_i
     raise KeyError(kernel)
 
 
+# ---------------------------------------------------------------------------
+# The operators around the recurrence
+# ---------------------------------------------------------------------------
+def _row_stride(name, t, inner=1):
+    """Elements from one row to the next of a tensor whose last `inner`
+    dimensions are one dense row and whose leading ones step evenly (a
+    contiguous tensor, or a slice of a joint projection)."""
+    row = 1
+    for size, stride in zip(reversed(t.shape[t.dim() - inner:]), reversed(t.stride()[t.dim() - inner:])):
+        if size != 1 and stride != row:
+            raise ValueError(f"{name}: the elements of a row must be adjacent")
+        row *= size
+    if t.numel() == 0:
+        return row
+    want = None
+    for size, stride in zip(reversed(t.shape[:t.dim() - inner]), reversed(t.stride()[:t.dim() - inner])):
+        if size == 1:
+            continue
+        if want is None:
+            step, want = stride, stride
+        if stride != want:
+            raise ValueError(f"{name}: the rows must be evenly spaced")
+        want = stride * size
+    if want is None:
+        return row
+    if step < row:
+        raise ValueError(f"{name}: rows overlap")
+    return step
+
+
+def _check_rows(device, contiguous, rows):
+    """All on `device`; the tensors of `contiguous` (name, tensor) are dense.
+    ``rows`` = (name, tensor, inner dimensions) may have evenly spaced rows:
+    returns their strides."""
+    strides = []
+    for name, t in contiguous:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for name, t, inner in rows:
+        strides.append(0 if t is None else _row_stride(name, t, inner))
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for name, t in list(contiguous) + [(n, t) for n, t, _ in rows]:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on different devices ({device} and {name} on {t.device})")
+    return strides
+
+
+def _expect(name, t, dtype, shape):
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if t is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_ACT = (torch.bfloat16, torch.float32)
+
+
+def _activation(name, t):
+    if t.dtype not in _ACT:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _workspace(need, workspace, device):
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _norm_args(x, weight, residual, s):
+    _activation("x", x)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    _expect("weight", weight, _ACT, (D,))
+    _expect("residual", residual, x.dtype, x.shape)
+    _expect("s", s, x.dtype, x.shape)
+    return D, x.numel() // max(D, 1)
+
+
+def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=None, s=None):
+    """Root-mean-square norm over the last dimension with the residual's
+    addition: s = x (+ residual), y = s / sqrt(mean(s^2) + eps) * weight.
+    x: [..., D] bf16 or fp32 (rows may be slices of wider ones); weight: [D]
+    bf16 or fp32; residual: as x, or None.  Returns (y, s) in x's dtype, s None
+    without a residual.  y may be x and s may be residual."""
+    lib = load_library()
+    D, rows = _norm_args(x, weight, residual, s)
+    _expect("y", y, x.dtype, x.shape)
+    (xs,) = _check_rows(x.device, [("weight", weight), ("residual", residual), ("y", y), ("s", s)], [("x", x, 1)])
+    with torch.cuda.device(x.device):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+        if s is None and residual is not None:
+            s = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        st = lib.kda_rms_norm_fwd(_ptr(x), xs, _ptr(residual), _ptr(weight), _dtype_code(weight), _ptr(y), _ptr(s),
+                                  rows, D, eps, _dtype_code(x), _stream_handle(x.device))
+    _check(st)
+    return y, s
+
+
+def rms_norm_quant_fwd(x, weight, residual=None, eps=1e-6, group=0, s=None):
+    """rms_norm_fwd with an e4m3 output: scale = max(amax |y|, 1e-10) / 448 over
+    each group of `group` columns (32, 64 or 128; 0: the whole row), q = y /
+    scale.  Returns (q [..., D] float8_e4m3fn, scale [..., D / group] fp32, s)."""
+    lib = load_library()
+    D, rows = _norm_args(x, weight, residual, s)
+    group = int(group)
+    if group < 0 or (group and D % group):
+        raise ValueError(f"group={group} must be 0 or divide D={D}")
+    (xs,) = _check_rows(x.device, [("weight", weight), ("residual", residual), ("s", s)], [("x", x, 1)])
+    with torch.cuda.device(x.device):
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty((*x.shape[:-1], D // group if group else 1), dtype=torch.float32, device=x.device)
+        if s is None and residual is not None:
+            s = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        st = lib.kda_rms_norm_quant_fwd(_ptr(x), xs, _ptr(residual), _ptr(weight), _dtype_code(weight), _ptr(q),
+                                        _ptr(scale), _ptr(s), rows, D, group, eps, _dtype_code(x),
+                                        _stream_handle(x.device))
+    _check(st)
+    return q, scale, s
+
+
+def rms_norm_bwd(dy, s, weight, ds=None, eps=1e-6, dx=None, workspace=None):
+    """Backward of rms_norm_fwd: dy and s (as the forward returned it; x without
+    a residual) [..., D]; ds, the gradient that reaches s past the norm, or None.
+    Returns a dict: dx (the gradient of x and of residual, ds included; may be
+    dy or ds) and dweight [D] fp32."""
+    lib = load_library()
+    D, rows = _norm_args(s, weight, None, dx)
+    _expect("dy", dy, s.dtype, s.shape)
+    _expect("ds", ds, s.dtype, s.shape)
+    _check_rows(s.device, [("dy", dy), ("s", s), ("weight", weight), ("ds", ds), ("dx", dx)], [])
+    with torch.cuda.device(s.device):
+        dx = torch.empty(s.shape, dtype=s.dtype, device=s.device) if dx is None else dx
+        dweight = torch.empty(D, dtype=torch.float32, device=s.device)
+        workspace, ws_bytes = _workspace(int(lib.kda_rms_norm_bwd_workspace_size(rows, D)), workspace, s.device)
+        st = lib.kda_rms_norm_bwd(_ptr(dy), _ptr(s), _ptr(weight), _dtype_code(weight), _ptr(ds), _ptr(dx),
+                                  _ptr(dweight), rows, D, eps, _dtype_code(s), _ptr(workspace), ws_bytes,
+                                  _stream_handle(s.device))
+    _check(st)
+    return dict(dx=dx, dweight=dweight)
+
+
+def _sequences(x, cu_seqlens):
+    """(B, T, num_seqs, N) of x [B, T, ...] and the packed table."""
+    B, T = x.shape[:2]
+    if cu_seqlens is None:
+        return B, T, 0, B
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise TypeError("cu_seqlens must be a 1-D int32 tensor of num_seqs + 1 entries")
+    if B != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B == 1")
+    n = cu_seqlens.numel() - 1
+    return B, T, n, n
+
+
+def _conv_args(x, weight, bias):
+    _activation("x", x)
+    D = x.shape[-1]
+    if weight.dim() != 2 or weight.shape[0] != D or not 2 <= weight.shape[1] <= 4:
+        raise ValueError(f"weight must be [D={D}, W] with W 2, 3 or 4, got {tuple(weight.shape)}")
+    _expect("weight", weight, _ACT, weight.shape)
+    _expect("bias", bias, weight.dtype, (D,))
+    return D, weight.shape[1]
+
+
+def short_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, output_final_state=True, y=None,
+                   state_out=None):
+    """Short causal depthwise convolution with SiLU: x [B,T,D] (a slice of a
+    joint projection may be given), weight [D,W] with W 2 to 4, bias [D] or None,
+    state [N,W-1,D] or None (the inputs before each sequence), cu_seqlens int32
+    [N+1] (B == 1) or None.  Returns (y [B,T,D], state_out [N,W-1,D], None when
+    output_final_state is False)."""
+    lib = load_library()
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B,T,D], got {tuple(x.shape)}")
+    D, W = _conv_args(x, weight, bias)
+    B, T, num_seqs, N = _sequences(x, cu_seqlens)
+    _expect("state", state, x.dtype, (N, W - 1, D))
+    _expect("state_out", state_out, x.dtype, (N, W - 1, D))
+    _expect("y", y, x.dtype, x.shape)
+    (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("cu_seqlens", cu_seqlens),
+                                   ("y", y), ("state_out", state_out)], [("x", x, 1)])
+    with torch.cuda.device(x.device):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+        if state_out is None and output_final_state:
+            state_out = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
+        st = lib.kda_short_conv_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _dtype_code(weight), _ptr(state), _ptr(y),
+                                    _ptr(state_out), _ptr(cu_seqlens), num_seqs, B, T, D, W, _dtype_code(x),
+                                    _stream_handle(x.device))
+    _check(st)
+    return y, state_out
+
+
+def short_conv_step(x, weight, state, bias=None, state_out=None, y=None):
+    """One token per sequence: x [N,D], state [N,W-1,D], updated in place unless
+    state_out is given.  Returns y [N,D]."""
+    lib = load_library()
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N,D], got {tuple(x.shape)}")
+    D, W = _conv_args(x, weight, bias)
+    N = x.shape[0]
+    _expect("state", state, x.dtype, (N, W - 1, D))
+    _expect("state_out", state_out, x.dtype, (N, W - 1, D))
+    _expect("y", y, x.dtype, x.shape)
+    (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("y", y),
+                                   ("state_out", state_out)], [("x", x, 1)])
+    with torch.cuda.device(x.device):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+        st = lib.kda_short_conv_step(_ptr(x), xs, _ptr(weight), _ptr(bias), _dtype_code(weight), _ptr(state), _ptr(y),
+                                     _ptr(state if state_out is None else state_out), N, D, W, _dtype_code(x),
+                                     _stream_handle(x.device))
+    _check(st)
+    return y
+
+
+def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, cu_seqlens=None, workspace=None):
+    """Backward of short_conv_fwd: dy [B,T,D] in x's dtype or fp32, dstate
+    [N,W-1,D] fp32 (the gradient of state_out) or None.  Returns a dict: dx in
+    x's dtype, dweight [D,W], dbias [D] (None without a bias) and dinit [N,W-1,D]
+    (the gradient of state), fp32."""
+    lib = load_library()
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B,T,D], got {tuple(x.shape)}")
+    D, W = _conv_args(x, weight, bias)
+    B, T, num_seqs, N = _sequences(x, cu_seqlens)
+    _expect("dy", dy, (x.dtype, torch.float32), x.shape)
+    _expect("state", state, x.dtype, (N, W - 1, D))
+    _expect("dstate", dstate, torch.float32, (N, W - 1, D))
+    (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("cu_seqlens", cu_seqlens),
+                                   ("dy", dy), ("dstate", dstate)], [("x", x, 1)])
+    f32 = dict(dtype=torch.float32, device=x.device)
+    with torch.cuda.device(x.device):
+        out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device), dweight=torch.empty((D, W), **f32),
+                   dbias=None if bias is None else torch.empty(D, **f32), dinit=torch.empty((N, W - 1, D), **f32))
+        workspace, ws_bytes = _workspace(int(lib.kda_short_conv_bwd_workspace_size(B, T, D, W)), workspace, x.device)
+        st = lib.kda_short_conv_bwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _dtype_code(weight), _ptr(state), _ptr(dy),
+                                    _dtype_code(dy), _ptr(dstate), _ptr(out["dx"]), _ptr(out["dweight"]),
+                                    _ptr(out["dbias"]), _ptr(out["dinit"]), _ptr(cu_seqlens), num_seqs, B, T, D, W,
+                                    _dtype_code(x), _ptr(workspace), ws_bytes, _stream_handle(x.device))
+    _check(st)
+    return out
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, lead):
+    _activation("x", x)
+    if x.dim() != lead + 1:
+        raise ValueError(f"x must have {lead + 1} dimensions, got {tuple(x.shape)}")
+    d = x.shape[-1]
+    if A.dim() != 2 or A.shape[0] != d:
+        raise ValueError(f"A must be [d={d}, S], got {tuple(A.shape)}")
+    S = A.shape[1]
+    _expect("A", A, torch.float32, A.shape)
+    _expect("dt", dt, x.dtype, x.shape)
+    _expect("z", z, x.dtype, x.shape)
+    if B.dim() != lead + 2:
+        raise ValueError(f"B must be [..., groups, S], got {tuple(B.shape)}")
+    groups = B.shape[-2]
+    if groups < 1 or d % groups:
+        raise ValueError(f"the groups of B and C ({groups}) must divide d={d}")
+    for name, t in (("B", B), ("C", C)):
+        _expect(name, t, x.dtype, (*x.shape[:-1], groups, S))
+    _expect("D", D, torch.float32, (d,))
+    _expect("dt_bias", dt_bias, torch.float32, (d,))
+    return d, S, groups
+
+
+def _scan_ptrs(x, dt, A, B, C, D, z, dt_bias, state, strides):
+    xs, dts, zs, bs, cs = strides
+    return (_ptr(x), xs, _ptr(dt), dts, _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D), _ptr(z), zs, _ptr(dt_bias),
+            _ptr(state))
+
+
+def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu_seqlens=None,
+                       output_final_state=True, y=None, S_out=None, workspace=None):
+    """Selective state space scan: h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,
+    y_t = (C_t . h_t + D x_t) silu(z_t), delta_t = softplus(dt_t + dt_bias).
+    x, dt, z: [B,T,d] bf16 or fp32; A: [d,S] fp32, S 8, 16, 32 or 64; B, C:
+    [B,T,groups,S] in x's dtype; D, dt_bias: [d] fp32 or None; S0: [N,d,S] fp32
+    or None; cu_seqlens: int32 [N+1] (B == 1) or None.  x, dt, z, B and C may be
+    slices of a joint projection.  Returns (y [B,T,d], S_out [N,d,S] fp32, None
+    when output_final_state is False)."""
+    lib = load_library()
+    d, S, groups = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    nb, T, num_seqs, N = _sequences(x, cu_seqlens)
+    _expect("S0", S0, torch.float32, (N, d, S))
+    _expect("S_out", S_out, torch.float32, (N, d, S))
+    _expect("y", y, x.dtype, x.shape)
+    strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S0", S0), ("cu_seqlens", cu_seqlens),
+                                     ("y", y), ("S_out", S_out)],
+                          [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
+    with torch.cuda.device(x.device):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+        if S_out is None and output_final_state:
+            S_out = torch.empty((N, d, S), dtype=torch.float32, device=x.device)
+        need = int(lib.kda_selective_scan_fwd_workspace_size(nb, T, d, S, groups, num_seqs))
+        workspace, ws_bytes = _workspace(need, workspace, x.device)
+        st = lib.kda_selective_scan_fwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _ptr(y), _ptr(S_out),
+                                        _ptr(cu_seqlens), num_seqs, nb, T, d, S, groups, _dtype_code(x),
+                                        _ptr(workspace), ws_bytes, _stream_handle(x.device))
+    _check(st)
+    return y, S_out
+
+
+def selective_scan_step(x, dt, A, B, C, S, D=None, z=None, dt_bias=None, S_out=None, y=None):
+    """One token per sequence: x, dt, z [N,d]; B, C [N,groups,S]; the state S
+    [N,d,S] fp32 is updated in place unless S_out is given.  Returns y [N,d]."""
+    lib = load_library()
+    d, ns, groups = _scan_args(x, dt, A, B, C, D, z, dt_bias, 1)
+    N = x.shape[0]
+    _expect("S", S, torch.float32, (N, d, ns))
+    _expect("S_out", S_out, torch.float32, (N, d, ns))
+    _expect("y", y, x.dtype, x.shape)
+    strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S", S), ("S_out", S_out), ("y", y)],
+                          [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
+    with torch.cuda.device(x.device):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+        st = lib.kda_selective_scan_step(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S, strides), _ptr(y),
+                                         _ptr(S if S_out is None else S_out), N, d, ns, groups, _dtype_code(x),
+                                         _stream_handle(x.device))
+    _check(st)
+    return y
+
+
+def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, S0=None, dS=None, cu_seqlens=None,
+                       workspace=None):
+    """Backward of selective_scan_fwd, given dy [B,T,d] in x's dtype and dS
+    [N,d,S] fp32 (the gradient of S_out) or None.  Returns a dict: dx, ddt, dz in
+    x's dtype (dz None without z) and, fp32, dA [d,S], dB, dC [B,T,groups,S], dD,
+    ddt_bias [d] (None without D, dt_bias) and dS0 [N,d,S]."""
+    lib = load_library()
+    d, S, groups = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    nb, T, num_seqs, N = _sequences(x, cu_seqlens)
+    _expect("dy", dy, x.dtype, x.shape)
+    _expect("S0", S0, torch.float32, (N, d, S))
+    _expect("dS", dS, torch.float32, (N, d, S))
+    strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S0", S0), ("dS", dS), ("dy", dy),
+                                     ("cu_seqlens", cu_seqlens)],
+                          [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
+    f32 = dict(dtype=torch.float32, device=x.device)
+    act = dict(dtype=x.dtype, device=x.device)
+    with torch.cuda.device(x.device):
+        out = dict(dx=torch.empty(x.shape, **act), ddt=torch.empty(x.shape, **act),
+                   dz=None if z is None else torch.empty(x.shape, **act), dA=torch.empty((d, S), **f32),
+                   dB=torch.empty(B.shape, **f32), dC=torch.empty(B.shape, **f32),
+                   dD=None if D is None else torch.empty(d, **f32),
+                   ddt_bias=None if dt_bias is None else torch.empty(d, **f32), dS0=torch.empty((N, d, S), **f32))
+        need = int(lib.kda_selective_scan_bwd_workspace_size(nb, T, d, S, groups))
+        workspace, ws_bytes = _workspace(need, workspace, x.device)
+        st = lib.kda_selective_scan_bwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _ptr(dy), _ptr(dS),
+                                        _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
+                                        _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]),
+                                        _ptr(out["dS0"]), _ptr(cu_seqlens), num_seqs, nb, T, d, S, groups,
+                                        _dtype_code(x), _ptr(workspace), ws_bytes, _stream_handle(x.device))
+    _check(st)
+    return out
+
+
 def version() -> int:
     return int(load_library().kda_version())
 
@@ -640,5 +1039,7 @@ def version() -> int:
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "recurrent_step", "chunk_fwd_host", "HostPrefill", "workspace_size",
            "launches_per_chunk_fwd", "kernel_names", "profile_chunk_fwd", "algorithmic_bytes_per_launch",
            "set_local_kernel", "uses_ws_kernel", "chunk_fwd_kernel_sequence", "set_prefill_path",
-           "prefill_phases", "uses_fused_kernel",
+           "prefill_phases", "uses_fused_kernel", "rms_norm_fwd", "rms_norm_quant_fwd", "rms_norm_bwd",
+           "short_conv_fwd", "short_conv_step", "short_conv_bwd", "selective_scan_fwd", "selective_scan_step",
+           "selective_scan_bwd",
            "last_error", "device_error", "version", "load_library", "lib_path", "KDAError", "EXPORTED"]

@@ -11,12 +11,12 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libkda.so")
 CSRC = os.path.join(PKG, "csrc")
-MAIN = os.path.join(CSRC, "kda_api.cu")
+UNITS = [os.path.join(CSRC, "kda_api.cu"), os.path.join(CSRC, "kda_layer_api.cu")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "-Xptxas", "-warn-spills",
     "--expt-relaxed-constexpr",
 ]
@@ -24,7 +24,7 @@ NVCC_FLAGS = [
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + [os.path.join(ROOT, "include", "kda.h")])
+                  + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "kda.h")])
 
 
 def needs_build() -> bool:
@@ -39,10 +39,24 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-o", tmp, MAIN]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    objects = [f"{tmp}.{i}.o" for i in range(len(UNITS))]
+    compiles = [[nvcc, *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-c", "-o", o, u]
+                for o, u in zip(objects, UNITS)]
+    try:
+        running = []
+        for cmd in compiles:
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append(subprocess.Popen(cmd))
+        codes = [p.wait() for p in running]
+        for cmd, code in zip(compiles, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.run([nvcc, *NVCC_FLAGS[:2], "-shared", "-o", tmp, *objects], check=True)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB)
     return LIB
 

@@ -12,6 +12,7 @@
 #include "kda_common.cuh"
 #include "kda_decode.cuh"
 #include "kda_host.cuh"
+#include "kda_status.h"
 
 namespace {
 
@@ -203,6 +204,17 @@ kda_status_t recurrent_step_impl(const char* fn, const void* q, const void* k, c
 }
 
 }  // namespace
+
+namespace kda {
+kda_status_t set_status(kda_status_t st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(t_err, sizeof(t_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
+void clear_status() { t_err[0] = 0; }
+}  // namespace kda
 
 extern "C" {
 
@@ -758,6 +770,10 @@ kda_status_t kda_device_error(int* code, cudaStream_t stream) {
   const int zero = 0;
   e = cudaMemcpyToSymbol(kda::g_device_error, &zero, sizeof(int));
   if (e != cudaSuccess) return cuda_fail(e, "kda_device_error: clear");
+  int layer = 0;
+  e = kda::take_layer_device_error(&layer);
+  if (e != cudaSuccess) return cuda_fail(e, "kda_device_error: layer kernels");
+  if (h == 0) h = layer;
   *code = h;
   return KDA_OK;
 }

@@ -44,8 +44,9 @@ inline int current_sm_count() {
 }
 
 // Device-side error word.  Bounded waits set it (never trap) when they give
-// up; the host reads and clears it through kda_device_error().
-__device__ int g_device_error;
+// up; the host reads and clears it through kda_device_error().  One word per
+// translation unit.
+static __device__ int g_device_error;
 
 // Codes match kda_status_t: a malformed cu_seqlens table seen on the device
 // (KDA_ERR_INVALID_ARG), a bounded wait that gave up (KDA_ERR_DEVICE_TIMEOUT).

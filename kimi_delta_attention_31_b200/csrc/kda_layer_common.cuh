@@ -1,0 +1,183 @@
+// kda_layer_common.cuh -- device helpers shared by the kernels around the
+// recurrence (norm, short convolution, selective scan): vector loads and
+// stores with conversion, which packed sequence a token belongs to, and the
+// sum of partial lines that makes every gradient of a shared weight
+// independent of scheduling.
+#pragma once
+#include "kda_common.cuh"
+
+namespace kda {
+
+// VEC elements of T in one access (VEC * sizeof(T) bytes, that aligned).
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+  T v[VEC];
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T* p) {
+  return *reinterpret_cast<const Pack<T, VEC>*>(p);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pack(T* p, const float (&x)[VEC]) {
+  Pack<T, VEC> o;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) o.v[i] = from_f32<T>(x[i]);
+  *reinterpret_cast<Pack<T, VEC>*>(p) = o;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Pack<T, VEC>& p, float (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) x[i] = to_f32<T>(p.v[i]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void load_f32(const T* p, float (&x)[VEC]) {
+  unpack<T, VEC>(load_pack<T, VEC>(p), x);
+}
+// VEC floats, 16 bytes an access where VEC allows it.
+template <int VEC>
+__device__ __forceinline__ void load_floats(const float* p, float (&x)[VEC]) {
+  constexpr int STEP = VEC >= 4 ? 4 : VEC;
+#pragma unroll
+  for (int i = 0; i < VEC; i += STEP) {
+    const Pack<float, STEP> v = load_pack<float, STEP>(p + i);
+#pragma unroll
+    for (int e = 0; e < STEP; ++e) x[i + e] = v.v[e];
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_floats(float* p, const float (&x)[VEC]) {
+  constexpr int STEP = VEC >= 4 ? 4 : VEC;
+#pragma unroll
+  for (int i = 0; i < VEC; i += STEP) {
+    Pack<float, STEP> v;
+#pragma unroll
+    for (int e = 0; e < STEP; ++e) v.v[e] = x[i + e];
+    *reinterpret_cast<Pack<float, STEP>*>(p + i) = v;
+  }
+}
+// VEC elements from element i of a parameter (weight, bias) whose type is a
+// run-time choice; i * (2 or 4) bytes must suit the vector.
+template <int VEC>
+__device__ __forceinline__ void load_param(const void* p, int is_bf16, long long i, float (&out)[VEC]) {
+  if (is_bf16) load_f32<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(p) + i, out);
+  else load_floats<VEC>(static_cast<const float*>(p) + i, out);
+}
+
+// The sequences of a call: packed (cu != nullptr, num of them over `total`
+// tokens) or num rows of T tokens each.
+struct Seqs {
+  const int32_t* cu;
+  int num;
+  long long T, total;
+};
+
+// The sequence token t (0 <= t < total) belongs to: the last one that starts
+// at or before t.  Always in [0, num), whatever the table holds.
+__device__ __forceinline__ int seq_of_token(const Seqs& q, long long t) {
+  if (!q.cu) return (int)(t / q.T);
+  int lo = 0, hi = q.num - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)q.cu[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ long long seq_start(const Seqs& q, int n) { return q.cu ? (long long)q.cu[n] : n * q.T; }
+__device__ __forceinline__ long long seq_end(const Seqs& q, int n) {
+  return q.cu ? (long long)q.cu[n + 1] : (n + 1) * q.T;
+}
+__device__ __forceinline__ bool seq_empty(const Seqs& q, int n) { return seq_end(q, n) <= seq_start(q, n); }
+
+// Raises the device error word if the packed table is not 0 .. total,
+// non-decreasing.  The threads of one CTA call it.  The kernels stay inside
+// the buffers with any table: token indices come from the grid, sequence
+// indices from seq_of_token.
+__device__ __forceinline__ void check_seq_table(const Seqs& q) {
+  if (!q.cu) return;
+  bool bad = threadIdx.x == 0 && (q.cu[0] != 0 || (long long)q.cu[q.num] != q.total);
+  for (int n = threadIdx.x; n < q.num; n += blockDim.x) bad |= q.cu[n + 1] < q.cu[n];
+  if (bad) raise_device_error(kDevErrBadSeqlens);
+}
+
+constexpr float kLog2eF = 1.4426950408889634f;
+constexpr float kLn2F = 0.6931471805599453f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + e^-x); 0 and 1 at the ends (the reciprocal of infinity is 0).
+__device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.f + ex2(-x * kLog2eF)); }
+
+// max that keeps NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 dup2(float a) { return make_float2(a, a); }
+
+// Column sums of `lines` rows of src, `cols` wide, each in row order within 8
+// slices: columns below `split` go to dst0, the rest to dst1 (either may be
+// null: not written).
+__global__ void __launch_bounds__(256) kda_sum_lines_kernel(const float* __restrict__ src, float* __restrict__ dst0,
+                                                            float* __restrict__ dst1, long long split, int lines,
+                                                            long long cols) {
+  __shared__ float s[8][32];
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const long long c = (long long)blockIdx.x * 32 + l;
+  float acc = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int i = w; i < lines; i += 8) acc += src[(long long)i * cols + c];
+  }
+  s[w][l] = acc;
+  __syncthreads();
+  if (w == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) acc += s[i][l];
+    if (c < split) {
+      if (dst0) dst0[c] = acc;
+    } else if (dst1) {
+      dst1[c - split] = acc;
+    }
+  }
+}
+inline cudaError_t launch_sum_lines(const float* src, float* dst0, float* dst1, long long split, int lines,
+                                    long long cols, cudaStream_t st) {
+  if (cols <= 0) return cudaSuccess;
+  kda_sum_lines_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, st>>>(src, dst0, dst1, split, lines, cols);
+  return cudaGetLastError();
+}
+
+}  // namespace kda

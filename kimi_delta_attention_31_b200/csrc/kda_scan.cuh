@@ -1,0 +1,403 @@
+// kda_scan.cuh -- selective state space scan: the diagonal sibling of the
+// recurrence, one state row of S numbers per channel.
+//
+//   delta_t = softplus(dt_t + dt_bias);  h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t
+//   y_t = (C_t . h_t + D x_t) silu(z_t)
+//
+// Forward: a thread owns one channel and SPT of its S states (S <= 16: all of
+// them) and walks the tokens with the state in registers; B and C of kTile
+// tokens sit in shared memory in fp32, shared by the channels of the CTA; the
+// tile after is loaded meanwhile.  One exponential per (token, channel, state)
+// bounds it (16 a clock and SM), not HBM: 8 bytes per token and channel.
+//
+// When a batch has too few channels to fill the card, or sequences are packed
+// (their lengths are on the device only), the token axis is cut into chunks
+// wherever they fall: kda_scan_local_kernel runs every chunk from a zero state,
+// kda_scan_carry_kernel chains the chunks (h is linear in the state that enters:
+// a whole chunk multiplies it by exp(A sum delta)), and the scan then runs each
+// chunk from its entry state.  A chunk in which a sequence starts passes
+// nothing on from before it.
+#pragma once
+#include "kda_layer_common.cuh"
+
+namespace kda {
+namespace scan {
+
+constexpr int kThreads = 128;
+constexpr int kTile = 8;  // tokens staged at a time
+
+struct Args {
+  const void *x, *dt, *z, *B, *C;
+  long long xs, dts, zs, bs, cs;  // elements from one token to the next
+  const float *A, *Dv, *dt_bias;  // [d, S], [d] or nullptr, [d] or nullptr
+  const float* S0;                // [N, d, S] or nullptr (zeros)
+  void* y;                        // [tokens, d]
+  float* S_out;                   // [N, d, S] or nullptr
+  Seqs q;
+  int d, cpg, blocks_per_group, ncb;  // channels, channels a group, CTAs' channel blocks
+  long long L;                        // tokens a chunk
+  long long chunks;
+  float* entry;  // [chunks, d, S]: local end states, then the states that enter
+  float* sumd;   // [chunks, d]: sum of delta, or -1 where a sequence starts in the chunk
+  // backward only
+  const void* dy;    // [tokens, d]
+  const float* dS;   // [N, d, S] or nullptr
+  float* exitg;      // [chunks, d, S]: as entry, for the gradient that comes from the right
+};
+
+template <int S>
+struct Shape {
+  static constexpr int SPT = S < 16 ? S : 16;   // states a thread
+  static constexpr int LPC = S / SPT;           // lanes a channel
+  static constexpr int CH = kThreads / LPC;     // channels a CTA
+};
+
+// log(1 + e^v), to fp32 accuracy also where it is small.
+__device__ __forceinline__ float softplus_f(float v) {
+  return fmaxf(v, 0.f) + log1pf(ex2(-fabsf(v) * kLog2eF));
+}
+
+template <int N>
+__device__ __forceinline__ void load_state(const float* p, float2 (&h)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(p + 2 * i);
+    h[i] = make_float2(v.x, v.y);
+    h[i + 1] = make_float2(v.z, v.w);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_state(float* p, const float2 (&h)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    *reinterpret_cast<float4*>(p + 2 * i) = make_float4(h[i].x, h[i].y, h[i + 1].x, h[i + 1].y);
+}
+template <int N>
+__device__ __forceinline__ void zero_state(float2 (&h)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) h[i] = make_float2(0.f, 0.f);
+}
+
+enum Mode : int { kForward = 0, kLocal = 1, kLocalBwd = 2 };
+
+// MODE kForward: the scan of each chunk from its entry state (S0 where a
+//   sequence starts).  kLocal: the end state of each chunk from zero and the sum
+//   of its deltas.  kLocalBwd: also the gradient that a chunk sends to the state
+//   before it, with nothing coming from its right:
+//     sum_t (prod_{s <= t} a_s) C_t dyy_t,  dyy = dy silu(z), up to the first
+//   sequence start in the chunk.
+template <typename T, int S, int MODE>
+__global__ void __launch_bounds__(kThreads) kda_selective_scan_kernel(const Args a) {
+  using Sh = Shape<S>;
+  constexpr int SPT = Sh::SPT, LPC = Sh::LPC, NP = SPT / 2;
+  constexpr bool kC = MODE != kLocal, kZ = MODE != kLocal;
+  constexpr int NBC = kTile * S / kThreads > 0 ? kTile * S / kThreads : 1;  // staged B (or C) elements a thread
+  __shared__ __align__(16) float sB[2][kTile][S];
+  __shared__ __align__(16) float sC[kC ? 2 : 1][kC ? kTile : 1][kC ? S : 4];
+
+  const int cb = (int)(blockIdx.x % a.ncb);
+  const long long chunk = blockIdx.x / a.ncb;
+  const int grp = cb / a.blocks_per_group;
+  const int cl = (cb % a.blocks_per_group) * Sh::CH + (int)threadIdx.x / LPC;
+  const int sl = (int)threadIdx.x % LPC;
+  const bool active = cl < a.cpg;
+  const int c = grp * a.cpg + (active ? cl : a.cpg - 1);
+  const long long crow = (long long)c * S + sl * SPT;
+
+  if (blockIdx.x == 0) check_seq_table(a.q);
+  if (MODE == kForward && chunk == 0 && a.S_out) {  // sequences without tokens keep their state
+    for (int n = 0; n < a.q.num; ++n)
+      if (seq_empty(a.q, n) && active) {
+        float2 v[NP];
+        if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, v);
+        else zero_state<NP>(v);
+        store_state<NP>(a.S_out + (long long)n * a.d * S + crow, v);
+      }
+  }
+  const long long t0 = chunk * a.L;
+  const long long t1 = t0 + a.L < a.q.total ? t0 + a.L : a.q.total;
+  if (t0 >= t1) return;
+
+  float2 A2[NP], h[NP];
+  load_state<NP>(a.A + crow, A2);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) A2[i] = mul2(A2[i], dup2(kLog2eF));
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+  const float Dc = kC && a.Dv ? a.Dv[c] : 0.f;
+
+  int n = seq_of_token(a.q, t0);
+  long long end = seq_end(a.q, n);
+  bool cut = seq_start(a.q, n) == t0;
+  if (cut && a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
+  else if (!cut && MODE == kForward && a.entry) load_state<NP>(a.entry + chunk * a.d * S + crow, h);
+  else zero_state<NP>(h);
+  float2 P[NP], R[NP];  // kLocalBwd: product of the decays so far, gradient sent to the left
+  if (MODE == kLocalBwd) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) P[i] = dup2(cut ? 0.f : 1.f), R[i] = dup2(0.f);
+  }
+  float sumd = 0.f;
+
+  const T* xp = static_cast<const T*>(a.x) + c;
+  const T* dtp = static_cast<const T*>(a.dt) + c;
+  const T* zp = static_cast<const T*>(a.z) + c;
+  const T* dyp = static_cast<const T*>(a.dy) + c;
+  const T* Bp = static_cast<const T*>(a.B) + (long long)grp * S;
+  const T* Cp = static_cast<const T*>(a.C) + (long long)grp * S;
+
+  T rx[kTile], rdt[kTile], rz[kTile], rdy[kTile], rB[NBC], rC[NBC];
+  auto fetch = [&](long long t) {
+#pragma unroll
+    for (int i = 0; i < NBC; ++i) {
+      const int e = i * kThreads + (int)threadIdx.x;
+      const long long tt = t + e / S < t1 ? t + e / S : t1 - 1;
+      if (e < kTile * S) {
+        rB[i] = Bp[tt * a.bs + e % S];
+        if (kC) rC[i] = Cp[tt * a.cs + e % S];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const long long tt = t + i < t1 ? t + i : t1 - 1;
+      rx[i] = xp[tt * a.xs];
+      rdt[i] = dtp[tt * a.dts];
+      if (kZ && a.z) rz[i] = zp[tt * a.zs];
+      if (MODE == kLocalBwd) rdy[i] = dyp[tt * a.d];
+    }
+  };
+  fetch(t0);
+  int buf = 0;
+  for (long long t = t0; t < t1; t += kTile, buf ^= 1) {
+#pragma unroll
+    for (int i = 0; i < NBC; ++i) {
+      const int e = i * kThreads + (int)threadIdx.x;
+      if (e < kTile * S) {
+        (&sB[buf][0][0])[e] = to_f32<T>(rB[i]);
+        if (kC) (&sC[kC ? buf : 0][0][0])[e] = to_f32<T>(rC[i]);
+      }
+    }
+    __syncthreads();  // the other buffer is free: its readers passed this point a tile ago
+    float xv[kTile], dv[kTile], gv[kTile], yv[kTile];
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      xv[i] = to_f32<T>(rx[i]);
+      dv[i] = softplus_f(to_f32<T>(rdt[i]) + bias);
+      if (kZ) {
+        const float zz = a.z ? to_f32<T>(rz[i]) : 0.f;
+        gv[i] = a.z ? zz * fast_sigmoid(zz) : 1.f;
+      }
+      if (MODE == kLocalBwd) gv[i] *= to_f32<T>(rdy[i]);
+    }
+    if (t + kTile < t1) fetch(t + kTile);
+    float part = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const long long ti = t + i;
+      if (ti < t1) {
+        if (ti == end) {  // the first token of another sequence
+          if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
+          n = seq_of_token(a.q, ti);
+          end = seq_end(a.q, n);
+          cut = true;
+          if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
+          else zero_state<NP>(h);
+          if (MODE == kLocalBwd) zero_state<NP>(P);
+        }
+        const float2 dd = dup2(dv[i]), uu = dup2(dv[i] * xv[i]);
+        const bool last = MODE == kLocalBwd && ti + 1 == end && a.dS;
+        float2 acc = dup2(0.f), acc1 = dup2(0.f);
+#pragma unroll
+        for (int p = 0; p < NP; p += 2) {
+          const float4 b4 = *reinterpret_cast<const float4*>(&sB[buf][i][sl * SPT + 2 * p]);
+          const float2 e0 = mul2(dd, A2[p]), e1 = mul2(dd, A2[p + 1]);
+          const float2 w0 = make_float2(ex2(e0.x), ex2(e0.y)), w1 = make_float2(ex2(e1.x), ex2(e1.y));
+          h[p] = fma2(w0, h[p], mul2(uu, make_float2(b4.x, b4.y)));
+          h[p + 1] = fma2(w1, h[p + 1], mul2(uu, make_float2(b4.z, b4.w)));
+          if (kC) {
+            const float4 c4 = *reinterpret_cast<const float4*>(&sC[kC ? buf : 0][kC ? i : 0][kC ? sl * SPT + 2 * p : 0]);
+            if (MODE == kForward) {
+              acc = fma2(h[p], make_float2(c4.x, c4.y), acc);
+              acc1 = fma2(h[p + 1], make_float2(c4.z, c4.w), acc1);
+            } else {
+              P[p] = mul2(P[p], w0);
+              P[p + 1] = mul2(P[p + 1], w1);
+              float2 g0 = mul2(dup2(gv[i]), make_float2(c4.x, c4.y)), g1 = mul2(dup2(gv[i]), make_float2(c4.z, c4.w));
+              if (last) {
+                const float4 s4 = *reinterpret_cast<const float4*>(a.dS + (long long)n * a.d * S + crow + 2 * p);
+                g0 = add2(g0, make_float2(s4.x, s4.y));
+                g1 = add2(g1, make_float2(s4.z, s4.w));
+              }
+              R[p] = fma2(P[p], g0, R[p]);
+              R[p + 1] = fma2(P[p + 1], g1, R[p + 1]);
+            }
+          }
+        }
+        part += dv[i];
+        if (MODE == kForward) {
+          acc = add2(acc, acc1);
+          float yy = acc.x + acc.y;
+#pragma unroll
+          for (int o = LPC / 2; o > 0; o >>= 1) yy += __shfl_xor_sync(0xffffffffu, yy, o);
+          yv[i] = fmaf(Dc, xv[i], yy) * gv[i];
+        }
+      }
+    }
+    sumd += part;
+    if (MODE == kForward && active && sl == 0) {
+      T* yp = static_cast<T*>(a.y) + c;
+#pragma unroll
+      for (int i = 0; i < kTile; ++i)
+        if (t + i < t1) yp[(t + i) * a.d] = from_f32<T>(yv[i]);
+    }
+  }
+  if (MODE == kForward) {
+    if (t1 == end && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
+  } else if (active) {
+    store_state<NP>(a.entry + chunk * a.d * S + crow, h);
+    if (MODE == kLocalBwd) store_state<NP>(a.exitg + chunk * a.d * S + crow, R);
+    if (sl == 0) a.sumd[chunk * a.d + c] = cut ? -1.f : sumd;
+  }
+}
+
+// Chains the chunks, one thread per (channel, state): entry[k] becomes the
+// state that enters chunk k, exitg[k] (blockIdx.y == 1) the gradient that
+// enters it from the right.
+__global__ void __launch_bounds__(128) kda_scan_carry_kernel(const float* __restrict__ A, float* entry, float* exitg,
+                                                             const float* __restrict__ sumd, int d, int S,
+                                                             long long chunks) {
+  constexpr int U = 8;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long row = (long long)d * S;
+  if (i >= row) return;
+  const int c = (int)(i / S);
+  const float A2 = A[i] * kLog2eF;
+  const bool rev = blockIdx.y == 1;
+  float* v = rev ? exitg : entry;
+  float h = 0.f;
+  for (long long k0 = 0; k0 < chunks; k0 += U) {
+    float loc[U], sd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < chunks) {
+        const long long k = rev ? chunks - 1 - k0 - u : k0 + u;
+        loc[u] = v[k * row + i];
+        sd[u] = sumd[k * d + c];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < chunks) {
+        const long long k = rev ? chunks - 1 - k0 - u : k0 + u;
+        v[k * row + i] = h;
+        h = sd[u] < 0.f ? loc[u] : fmaf(ex2(sd[u] * A2), h, loc[u]);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One token of each of N sequences.  Four states a lane; S_out may be S0.
+// HBM-bound: the state is read and written once.
+// ---------------------------------------------------------------------------
+template <typename T, int S>
+__global__ void __launch_bounds__(256) kda_selective_scan_step_kernel(const Args a) {
+  constexpr int LPC = S / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long rows = (long long)a.q.num * a.d;
+  const long long r = i / LPC;
+  const bool live = r < rows;
+  const long long rc = live ? r : rows - 1;
+  const long long n = rc / a.d;
+  const int c = (int)(rc - n * a.d), sl = (int)(i % LPC);
+  const int grp = c / a.cpg;
+  const float4 s4 = *reinterpret_cast<const float4*>(a.S0 + rc * S + sl * 4);
+  const float4 A4 = *reinterpret_cast<const float4*>(a.A + (long long)c * S + sl * 4);
+  const T* Bp = static_cast<const T*>(a.B) + n * a.bs + (long long)grp * S + sl * 4;
+  const T* Cp = static_cast<const T*>(a.C) + n * a.cs + (long long)grp * S + sl * 4;
+  const float xv = to_f32<T>(static_cast<const T*>(a.x)[n * a.xs + c]);
+  const float dv = to_f32<T>(static_cast<const T*>(a.dt)[n * a.dts + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
+  float zz = 0.f;
+  if (a.z) zz = to_f32<T>(static_cast<const T*>(a.z)[n * a.zs + c]);
+  float b[4], cc[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = to_f32<T>(Bp[e]), cc[e] = to_f32<T>(Cp[e]);
+  const float delta = softplus_f(dv), k = delta * kLog2eF, u = delta * xv;
+  float4 h;
+  h.x = fmaf(ex2(k * A4.x), s4.x, u * b[0]);
+  h.y = fmaf(ex2(k * A4.y), s4.y, u * b[1]);
+  h.z = fmaf(ex2(k * A4.z), s4.z, u * b[2]);
+  h.w = fmaf(ex2(k * A4.w), s4.w, u * b[3]);
+  float y = fmaf(h.x, cc[0], h.y * cc[1]) + fmaf(h.z, cc[2], h.w * cc[3]);
+#pragma unroll
+  for (int o = LPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+  if (!live) return;
+  *reinterpret_cast<float4*>(a.S_out + rc * S + sl * 4) = h;
+  if (sl == 0) {
+    if (a.Dv) y = fmaf(a.Dv[c], xv, y);
+    if (a.z) y *= zz * fast_sigmoid(zz);
+    static_cast<T*>(a.y)[rc] = from_f32<T>(y);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+inline bool supported_state(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }
+inline int lanes_per_channel(int S) { return S <= 16 ? 1 : S / 16; }
+inline int channel_blocks(int d, int groups, int S) {
+  const int ch = kThreads / lanes_per_channel(S);
+  return groups * ((d / groups + ch - 1) / ch);
+}
+
+// Chunks of the forward.  A batch whose channels give every SM sub-partition a
+// warp or more runs unsplit (a split costs the exponentials a second time);
+// otherwise, and for packed sequences, the token axis is cut so that about
+// 16 warps an SM run, into chunks of 64 tokens at least.
+struct FwdPlan {
+  bool split;
+  long long L, chunks;
+};
+inline FwdPlan fwd_plan(long long B, long long T, int num_seqs, int d, int groups, int S) {
+  const long long tokens = B * T;
+  const long long warps = (long long)channel_blocks(d, groups, S) * (kThreads / 32);
+  const bool packed = num_seqs > 1;
+  if (!packed && (B * warps >= 148 * 4 || T < 128)) return {false, T > 0 ? T : 1, B};
+  if (tokens < 128) return {false, tokens > 0 ? tokens : 1, 1};
+  long long chunks = (148 * 16 + warps - 1) / warps;
+  long long L = (tokens + chunks - 1) / chunks;
+  L = L < 64 ? 64 : (L + kTile - 1) / kTile * kTile;
+  chunks = (tokens + L - 1) / L;
+  return {chunks > 1, L, chunks};
+}
+inline size_t carry_floats(long long chunks, int d, int S) { return (size_t)chunks * d * S; }
+
+template <typename T, int S, int MODE>
+cudaError_t launch_scan(Args a, cudaStream_t st) {
+  const long long grid = a.chunks * a.ncb;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kda_selective_scan_kernel<T, S, MODE><<<(unsigned)grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+inline cudaError_t launch_carry(const Args& a, int S, bool both, cudaStream_t st) {
+  const long long row = (long long)a.d * S;
+  kda_scan_carry_kernel<<<dim3((unsigned)((row + 127) / 128), both ? 2 : 1), 128, 0, st>>>(a.A, a.entry, a.exitg,
+                                                                                          a.sumd, a.d, S, a.chunks);
+  return cudaGetLastError();
+}
+template <typename T, int S>
+cudaError_t launch_fwd(Args a, bool split, cudaStream_t st) {
+  if (split) {
+    cudaError_t e = launch_scan<T, S, kLocal>(a, st);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_carry(a, S, false, st)) != cudaSuccess) return e;
+  }
+  return launch_scan<T, S, kForward>(a, st);
+}
+template <typename T, int S>
+cudaError_t launch_step(const Args& a, cudaStream_t st) {
+  const long long grid = ((long long)a.q.num * a.d * (S / 4) + 255) / 256;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kda_selective_scan_step_kernel<T, S><<<(unsigned)grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace scan
+}  // namespace kda
