@@ -23,6 +23,7 @@ workspace_size(...), last_error(), device_error(), lib_path()
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -678,80 +679,111 @@ def _row_stride(name, t, inner=1):
     """Elements from one row to the next of a tensor whose last `inner`
     dimensions are one dense row and whose leading ones step evenly (a
     contiguous tensor, or a slice of a joint projection)."""
-    row = 1
-    for size, stride in zip(reversed(t.shape[t.dim() - inner:]), reversed(t.stride()[t.dim() - inner:])):
-        if size != 1 and stride != row:
-            raise ValueError(f"{name}: the elements of a row must be adjacent")
-        row *= size
-    if t.numel() == 0:
+    shape = t.shape
+    row = shape[-1] if inner == 1 else shape[-1] * shape[-2]
+    if t.is_contiguous():
         return row
-    want = None
-    for size, stride in zip(reversed(t.shape[:t.dim() - inner]), reversed(t.stride()[:t.dim() - inner])):
-        if size == 1:
+    strides = t.stride()
+    dense = 1
+    for i in range(1, inner + 1):
+        if shape[-i] != 1 and strides[-i] != dense:
+            raise ValueError(f"{name}: the elements of a row must be adjacent")
+        dense *= shape[-i]
+    step = want = None
+    for i in range(inner + 1, len(shape) + 1):
+        if shape[-i] == 1:
             continue
         if want is None:
-            step, want = stride, stride
-        if stride != want:
+            step = want = strides[-i]
+        if strides[-i] != want:
             raise ValueError(f"{name}: the rows must be evenly spaced")
-        want = stride * size
-    if want is None:
+        want = strides[-i] * shape[-i]
+    if step is None:
         return row
     if step < row:
         raise ValueError(f"{name}: rows overlap")
     return step
 
 
-def _check_rows(device, contiguous, rows):
-    """All on `device`; the tensors of `contiguous` (name, tensor) are dense.
-    ``rows`` = (name, tensor, inner dimensions) may have evenly spaced rows:
-    returns their strides."""
-    strides = []
-    for name, t in contiguous:
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    for name, t, inner in rows:
-        strides.append(0 if t is None else _row_stride(name, t, inner))
+def _check_dense(device, tensors):
+    """The (name, tensor or None) pairs are contiguous, on the CUDA device `device`."""
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    for name, t in list(contiguous) + [(n, t) for n, t, _ in rows]:
+    for name, t in tensors:
+        if t is not None:
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.device != device:
+                raise ValueError(f"tensors on different devices ({device} and {name} on {t.device})")
+
+
+def _check_rows(device, dense, rows):
+    """Checks `dense` as _check_dense does; ``rows`` = (name, tensor, inner
+    dimensions) may have evenly spaced rows: returns their strides."""
+    strides = [0 if t is None else _row_stride(name, t, inner) for name, t, inner in rows]
+    _check_dense(device, dense)
+    for name, t, _ in rows:
         if t is not None and t.device != device:
             raise ValueError(f"tensors on different devices ({device} and {name} on {t.device})")
     return strides
 
 
 def _expect(name, t, dtype, shape):
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    if t is not None and t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is None:
+        return
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
-_ACT = (torch.bfloat16, torch.float32)
+_ACT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 
 
-def _activation(name, t):
-    if t.dtype not in _ACT:
+def _act_code(name, t):
+    code = _ACT.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return code
 
 
-def _workspace(need, workspace, device):
-    if workspace is None and need:
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device made current for the call (nothing to do where it is)."""
+    return _SAME_DEVICE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _new_workspace(need, workspace, device):
+    if workspace is None:
+        if not need:
+            return None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _norm_args(x, weight, residual, s):
-    _activation("x", x)
-    if x.dim() < 1:
-        raise ValueError("x must be [..., D]")
+    code = _act_code("x", x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must be [..., D], got {tuple(x.shape)}")
     D = x.shape[-1]
-    _expect("weight", weight, _ACT, (D,))
+    wcode = _act_code("weight", weight)
+    if weight.shape != (D,):
+        raise ValueError(f"weight must be {(D,)}, got {tuple(weight.shape)}")
     _expect("residual", residual, x.dtype, x.shape)
     _expect("s", s, x.dtype, x.shape)
-    return D, x.numel() // max(D, 1)
+    return D, x.numel() // D, code, wcode
 
 
 def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=None, s=None):
@@ -760,16 +792,16 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=None, s=None):
     x: [..., D] bf16 or fp32 (rows may be slices of wider ones); weight: [D]
     bf16 or fp32; residual: as x, or None.  Returns (y, s) in x's dtype, s None
     without a residual.  y may be x and s may be residual."""
-    lib = load_library()
-    D, rows = _norm_args(x, weight, residual, s)
+    lib = _lib or load_library()
+    D, rows, code, wcode = _norm_args(x, weight, residual, s)
     _expect("y", y, x.dtype, x.shape)
     (xs,) = _check_rows(x.device, [("weight", weight), ("residual", residual), ("y", y), ("s", s)], [("x", x, 1)])
-    with torch.cuda.device(x.device):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+    with _on(x.device):
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
         if s is None and residual is not None:
-            s = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        st = lib.kda_rms_norm_fwd(_ptr(x), xs, _ptr(residual), _ptr(weight), _dtype_code(weight), _ptr(y), _ptr(s),
-                                  rows, D, eps, _dtype_code(x), _stream_handle(x.device))
+            s = torch.empty_like(x, memory_format=torch.contiguous_format)
+        st = lib.kda_rms_norm_fwd(_addr(x), xs, _addr(residual), _addr(weight), wcode, _addr(y), _addr(s),
+                                  rows, D, eps, code, _raw_stream(x.device))
     _check(st)
     return y, s
 
@@ -778,20 +810,20 @@ def rms_norm_quant_fwd(x, weight, residual=None, eps=1e-6, group=0, s=None):
     """rms_norm_fwd with an e4m3 output: scale = max(amax |y|, 1e-10) / 448 over
     each group of `group` columns (32, 64 or 128; 0: the whole row), q = y /
     scale.  Returns (q [..., D] float8_e4m3fn, scale [..., D / group] fp32, s)."""
-    lib = load_library()
-    D, rows = _norm_args(x, weight, residual, s)
+    lib = _lib or load_library()
+    D, rows, code, wcode = _norm_args(x, weight, residual, s)
     group = int(group)
     if group < 0 or (group and D % group):
         raise ValueError(f"group={group} must be 0 or divide D={D}")
     (xs,) = _check_rows(x.device, [("weight", weight), ("residual", residual), ("s", s)], [("x", x, 1)])
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
         scale = torch.empty((*x.shape[:-1], D // group if group else 1), dtype=torch.float32, device=x.device)
         if s is None and residual is not None:
-            s = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        st = lib.kda_rms_norm_quant_fwd(_ptr(x), xs, _ptr(residual), _ptr(weight), _dtype_code(weight), _ptr(q),
-                                        _ptr(scale), _ptr(s), rows, D, group, eps, _dtype_code(x),
-                                        _stream_handle(x.device))
+            s = torch.empty_like(x, memory_format=torch.contiguous_format)
+        st = lib.kda_rms_norm_quant_fwd(_addr(x), xs, _addr(residual), _addr(weight), wcode, _addr(q),
+                                        _addr(scale), _addr(s), rows, D, group, eps, code,
+                                        _raw_stream(x.device))
     _check(st)
     return q, scale, s
 
@@ -801,18 +833,18 @@ def rms_norm_bwd(dy, s, weight, ds=None, eps=1e-6, dx=None, workspace=None):
     a residual) [..., D]; ds, the gradient that reaches s past the norm, or None.
     Returns a dict: dx (the gradient of x and of residual, ds included; may be
     dy or ds) and dweight [D] fp32."""
-    lib = load_library()
-    D, rows = _norm_args(s, weight, None, dx)
+    lib = _lib or load_library()
+    D, rows, code, wcode = _norm_args(s, weight, None, dx)
     _expect("dy", dy, s.dtype, s.shape)
     _expect("ds", ds, s.dtype, s.shape)
-    _check_rows(s.device, [("dy", dy), ("s", s), ("weight", weight), ("ds", ds), ("dx", dx)], [])
-    with torch.cuda.device(s.device):
-        dx = torch.empty(s.shape, dtype=s.dtype, device=s.device) if dx is None else dx
+    _check_dense(s.device, (("dy", dy), ("s", s), ("weight", weight), ("ds", ds), ("dx", dx)))
+    with _on(s.device):
+        dx = torch.empty_like(s) if dx is None else dx
         dweight = torch.empty(D, dtype=torch.float32, device=s.device)
-        workspace, ws_bytes = _workspace(int(lib.kda_rms_norm_bwd_workspace_size(rows, D)), workspace, s.device)
-        st = lib.kda_rms_norm_bwd(_ptr(dy), _ptr(s), _ptr(weight), _dtype_code(weight), _ptr(ds), _ptr(dx),
-                                  _ptr(dweight), rows, D, eps, _dtype_code(s), _ptr(workspace), ws_bytes,
-                                  _stream_handle(s.device))
+        workspace, ws_bytes = _new_workspace(int(lib.kda_rms_norm_bwd_workspace_size(rows, D)), workspace, s.device)
+        st = lib.kda_rms_norm_bwd(_addr(dy), _addr(s), _addr(weight), wcode, _addr(ds), _addr(dx),
+                                  _addr(dweight), rows, D, eps, code, _addr(workspace), ws_bytes,
+                                  _raw_stream(s.device))
     _check(st)
     return dict(dx=dx, dweight=dweight)
 
@@ -831,13 +863,13 @@ def _sequences(x, cu_seqlens):
 
 
 def _conv_args(x, weight, bias):
-    _activation("x", x)
+    code = _act_code("x", x)
     D = x.shape[-1]
     if weight.dim() != 2 or weight.shape[0] != D or not 2 <= weight.shape[1] <= 4:
         raise ValueError(f"weight must be [D={D}, W] with W 2, 3 or 4, got {tuple(weight.shape)}")
-    _expect("weight", weight, _ACT, weight.shape)
+    wcode = _act_code("weight", weight)
     _expect("bias", bias, weight.dtype, (D,))
-    return D, weight.shape[1]
+    return D, weight.shape[1], code, wcode
 
 
 def short_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, output_final_state=True, y=None,
@@ -847,23 +879,23 @@ def short_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, output_fin
     state [N,W-1,D] or None (the inputs before each sequence), cu_seqlens int32
     [N+1] (B == 1) or None.  Returns (y [B,T,D], state_out [N,W-1,D], None when
     output_final_state is False)."""
-    lib = load_library()
+    lib = _lib or load_library()
     if x.dim() != 3:
         raise ValueError(f"x must be [B,T,D], got {tuple(x.shape)}")
-    D, W = _conv_args(x, weight, bias)
+    D, W, code, wcode = _conv_args(x, weight, bias)
     B, T, num_seqs, N = _sequences(x, cu_seqlens)
     _expect("state", state, x.dtype, (N, W - 1, D))
     _expect("state_out", state_out, x.dtype, (N, W - 1, D))
     _expect("y", y, x.dtype, x.shape)
     (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("cu_seqlens", cu_seqlens),
                                    ("y", y), ("state_out", state_out)], [("x", x, 1)])
-    with torch.cuda.device(x.device):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+    with _on(x.device):
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
         if state_out is None and output_final_state:
             state_out = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
-        st = lib.kda_short_conv_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _dtype_code(weight), _ptr(state), _ptr(y),
-                                    _ptr(state_out), _ptr(cu_seqlens), num_seqs, B, T, D, W, _dtype_code(x),
-                                    _stream_handle(x.device))
+        st = lib.kda_short_conv_fwd(_addr(x), xs, _addr(weight), _addr(bias), wcode, _addr(state), _addr(y),
+                                    _addr(state_out), _addr(cu_seqlens), num_seqs, B, T, D, W, code,
+                                    _raw_stream(x.device))
     _check(st)
     return y, state_out
 
@@ -871,21 +903,21 @@ def short_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, output_fin
 def short_conv_step(x, weight, state, bias=None, state_out=None, y=None):
     """One token per sequence: x [N,D], state [N,W-1,D], updated in place unless
     state_out is given.  Returns y [N,D]."""
-    lib = load_library()
+    lib = _lib or load_library()
     if x.dim() != 2:
         raise ValueError(f"x must be [N,D], got {tuple(x.shape)}")
-    D, W = _conv_args(x, weight, bias)
+    D, W, code, wcode = _conv_args(x, weight, bias)
     N = x.shape[0]
     _expect("state", state, x.dtype, (N, W - 1, D))
     _expect("state_out", state_out, x.dtype, (N, W - 1, D))
     _expect("y", y, x.dtype, x.shape)
     (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("y", y),
                                    ("state_out", state_out)], [("x", x, 1)])
-    with torch.cuda.device(x.device):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
-        st = lib.kda_short_conv_step(_ptr(x), xs, _ptr(weight), _ptr(bias), _dtype_code(weight), _ptr(state), _ptr(y),
-                                     _ptr(state if state_out is None else state_out), N, D, W, _dtype_code(x),
-                                     _stream_handle(x.device))
+    with _on(x.device):
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
+        st = lib.kda_short_conv_step(_addr(x), xs, _addr(weight), _addr(bias), wcode, _addr(state), _addr(y),
+                                     _addr(state if state_out is None else state_out), N, D, W, code,
+                                     _raw_stream(x.device))
     _check(st)
     return y
 
@@ -895,31 +927,33 @@ def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, cu_seqlens
     [N,W-1,D] fp32 (the gradient of state_out) or None.  Returns a dict: dx in
     x's dtype, dweight [D,W], dbias [D] (None without a bias) and dinit [N,W-1,D]
     (the gradient of state), fp32."""
-    lib = load_library()
+    lib = _lib or load_library()
     if x.dim() != 3:
         raise ValueError(f"x must be [B,T,D], got {tuple(x.shape)}")
-    D, W = _conv_args(x, weight, bias)
+    D, W, code, wcode = _conv_args(x, weight, bias)
     B, T, num_seqs, N = _sequences(x, cu_seqlens)
-    _expect("dy", dy, (x.dtype, torch.float32), x.shape)
+    if dy.dtype is not torch.float32:
+        _expect("dy", dy, x.dtype, x.shape)
+    _expect("dy", dy, dy.dtype, x.shape)
     _expect("state", state, x.dtype, (N, W - 1, D))
     _expect("dstate", dstate, torch.float32, (N, W - 1, D))
     (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("cu_seqlens", cu_seqlens),
                                    ("dy", dy), ("dstate", dstate)], [("x", x, 1)])
     f32 = dict(dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device), dweight=torch.empty((D, W), **f32),
+    with _on(x.device):
+        out = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format), dweight=torch.empty((D, W), **f32),
                    dbias=None if bias is None else torch.empty(D, **f32), dinit=torch.empty((N, W - 1, D), **f32))
-        workspace, ws_bytes = _workspace(int(lib.kda_short_conv_bwd_workspace_size(B, T, D, W)), workspace, x.device)
-        st = lib.kda_short_conv_bwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _dtype_code(weight), _ptr(state), _ptr(dy),
-                                    _dtype_code(dy), _ptr(dstate), _ptr(out["dx"]), _ptr(out["dweight"]),
-                                    _ptr(out["dbias"]), _ptr(out["dinit"]), _ptr(cu_seqlens), num_seqs, B, T, D, W,
-                                    _dtype_code(x), _ptr(workspace), ws_bytes, _stream_handle(x.device))
+        workspace, ws_bytes = _new_workspace(int(lib.kda_short_conv_bwd_workspace_size(B, T, D, W)), workspace, x.device)
+        st = lib.kda_short_conv_bwd(_addr(x), xs, _addr(weight), _addr(bias), wcode, _addr(state), _addr(dy),
+                                    _ACT[dy.dtype], _addr(dstate), _addr(out["dx"]), _addr(out["dweight"]),
+                                    _addr(out["dbias"]), _addr(out["dinit"]), _addr(cu_seqlens), num_seqs, B, T, D, W,
+                                    code, _addr(workspace), ws_bytes, _raw_stream(x.device))
     _check(st)
     return out
 
 
 def _scan_args(x, dt, A, B, C, D, z, dt_bias, lead):
-    _activation("x", x)
+    code = _act_code("x", x)
     if x.dim() != lead + 1:
         raise ValueError(f"x must have {lead + 1} dimensions, got {tuple(x.shape)}")
     d = x.shape[-1]
@@ -938,13 +972,13 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, lead):
         _expect(name, t, x.dtype, (*x.shape[:-1], groups, S))
     _expect("D", D, torch.float32, (d,))
     _expect("dt_bias", dt_bias, torch.float32, (d,))
-    return d, S, groups
+    return d, S, groups, code
 
 
 def _scan_ptrs(x, dt, A, B, C, D, z, dt_bias, state, strides):
     xs, dts, zs, bs, cs = strides
-    return (_ptr(x), xs, _ptr(dt), dts, _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D), _ptr(z), zs, _ptr(dt_bias),
-            _ptr(state))
+    return (_addr(x), xs, _addr(dt), dts, _addr(A), _addr(B), bs, _addr(C), cs, _addr(D), _addr(z), zs, _addr(dt_bias),
+            _addr(state))
 
 
 def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu_seqlens=None,
@@ -956,8 +990,8 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu
     or None; cu_seqlens: int32 [N+1] (B == 1) or None.  x, dt, z, B and C may be
     slices of a joint projection.  Returns (y [B,T,d], S_out [N,d,S] fp32, None
     when output_final_state is False)."""
-    lib = load_library()
-    d, S, groups = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    lib = _lib or load_library()
+    d, S, groups, code = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
     nb, T, num_seqs, N = _sequences(x, cu_seqlens)
     _expect("S0", S0, torch.float32, (N, d, S))
     _expect("S_out", S_out, torch.float32, (N, d, S))
@@ -965,15 +999,15 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu
     strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S0", S0), ("cu_seqlens", cu_seqlens),
                                      ("y", y), ("S_out", S_out)],
                           [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
-    with torch.cuda.device(x.device):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+    with _on(x.device):
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
         if S_out is None and output_final_state:
             S_out = torch.empty((N, d, S), dtype=torch.float32, device=x.device)
         need = int(lib.kda_selective_scan_fwd_workspace_size(nb, T, d, S, groups, num_seqs))
-        workspace, ws_bytes = _workspace(need, workspace, x.device)
-        st = lib.kda_selective_scan_fwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _ptr(y), _ptr(S_out),
-                                        _ptr(cu_seqlens), num_seqs, nb, T, d, S, groups, _dtype_code(x),
-                                        _ptr(workspace), ws_bytes, _stream_handle(x.device))
+        workspace, ws_bytes = _new_workspace(need, workspace, x.device)
+        st = lib.kda_selective_scan_fwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _addr(y), _addr(S_out),
+                                        _addr(cu_seqlens), num_seqs, nb, T, d, S, groups, code,
+                                        _addr(workspace), ws_bytes, _raw_stream(x.device))
     _check(st)
     return y, S_out
 
@@ -981,19 +1015,19 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu
 def selective_scan_step(x, dt, A, B, C, S, D=None, z=None, dt_bias=None, S_out=None, y=None):
     """One token per sequence: x, dt, z [N,d]; B, C [N,groups,S]; the state S
     [N,d,S] fp32 is updated in place unless S_out is given.  Returns y [N,d]."""
-    lib = load_library()
-    d, ns, groups = _scan_args(x, dt, A, B, C, D, z, dt_bias, 1)
+    lib = _lib or load_library()
+    d, ns, groups, code = _scan_args(x, dt, A, B, C, D, z, dt_bias, 1)
     N = x.shape[0]
     _expect("S", S, torch.float32, (N, d, ns))
     _expect("S_out", S_out, torch.float32, (N, d, ns))
     _expect("y", y, x.dtype, x.shape)
     strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S", S), ("S_out", S_out), ("y", y)],
                           [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
-    with torch.cuda.device(x.device):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
-        st = lib.kda_selective_scan_step(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S, strides), _ptr(y),
-                                         _ptr(S if S_out is None else S_out), N, d, ns, groups, _dtype_code(x),
-                                         _stream_handle(x.device))
+    with _on(x.device):
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
+        st = lib.kda_selective_scan_step(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S, strides), _addr(y),
+                                         _addr(S if S_out is None else S_out), N, d, ns, groups, code,
+                                         _raw_stream(x.device))
     _check(st)
     return y
 
@@ -1004,8 +1038,8 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, S0=None
     [N,d,S] fp32 (the gradient of S_out) or None.  Returns a dict: dx, ddt, dz in
     x's dtype (dz None without z) and, fp32, dA [d,S], dB, dC [B,T,groups,S], dD,
     ddt_bias [d] (None without D, dt_bias) and dS0 [N,d,S]."""
-    lib = load_library()
-    d, S, groups = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    lib = _lib or load_library()
+    d, S, groups, code = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
     nb, T, num_seqs, N = _sequences(x, cu_seqlens)
     _expect("dy", dy, x.dtype, x.shape)
     _expect("S0", S0, torch.float32, (N, d, S))
@@ -1014,20 +1048,19 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, S0=None
                                      ("cu_seqlens", cu_seqlens)],
                           [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
     f32 = dict(dtype=torch.float32, device=x.device)
-    act = dict(dtype=x.dtype, device=x.device)
-    with torch.cuda.device(x.device):
-        out = dict(dx=torch.empty(x.shape, **act), ddt=torch.empty(x.shape, **act),
-                   dz=None if z is None else torch.empty(x.shape, **act), dA=torch.empty((d, S), **f32),
+    with _on(x.device):
+        out = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format), ddt=torch.empty_like(x, memory_format=torch.contiguous_format),
+                   dz=None if z is None else torch.empty_like(x, memory_format=torch.contiguous_format), dA=torch.empty((d, S), **f32),
                    dB=torch.empty(B.shape, **f32), dC=torch.empty(B.shape, **f32),
                    dD=None if D is None else torch.empty(d, **f32),
                    ddt_bias=None if dt_bias is None else torch.empty(d, **f32), dS0=torch.empty((N, d, S), **f32))
         need = int(lib.kda_selective_scan_bwd_workspace_size(nb, T, d, S, groups))
-        workspace, ws_bytes = _workspace(need, workspace, x.device)
-        st = lib.kda_selective_scan_bwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _ptr(dy), _ptr(dS),
-                                        _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
-                                        _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]),
-                                        _ptr(out["dS0"]), _ptr(cu_seqlens), num_seqs, nb, T, d, S, groups,
-                                        _dtype_code(x), _ptr(workspace), ws_bytes, _stream_handle(x.device))
+        workspace, ws_bytes = _new_workspace(need, workspace, x.device)
+        st = lib.kda_selective_scan_bwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _addr(dy), _addr(dS),
+                                        _addr(out["dx"]), _addr(out["ddt"]), _addr(out["dA"]), _addr(out["dB"]),
+                                        _addr(out["dC"]), _addr(out["dD"]), _addr(out["dz"]), _addr(out["ddt_bias"]),
+                                        _addr(out["dS0"]), _addr(cu_seqlens), num_seqs, nb, T, d, S, groups,
+                                        code, _addr(workspace), ws_bytes, _raw_stream(x.device))
     _check(st)
     return out
 

@@ -147,25 +147,30 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 dup2(float a) { return make_float2(a, a); }
 
-// Column sums of `lines` rows of src, `cols` wide, each in row order within 8
+// Column sums of `lines` rows of src, `cols` wide, each in row order within 32
 // slices: columns below `split` go to dst0, the rest to dst1 (either may be
 // null: not written).
-__global__ void __launch_bounds__(256) kda_sum_lines_kernel(const float* __restrict__ src, float* __restrict__ dst0,
-                                                            float* __restrict__ dst1, long long split, int lines,
-                                                            long long cols) {
-  __shared__ float s[8][32];
+constexpr int kSumSlices = 32;
+__global__ void __launch_bounds__(32 * kSumSlices) kda_sum_lines_kernel(const float* __restrict__ src,
+                                                                        float* __restrict__ dst0,
+                                                                        float* __restrict__ dst1, long long split,
+                                                                        int lines, long long cols) {
+  __shared__ float s[kSumSlices][33];
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long c = (long long)blockIdx.x * 32 + l;
+  const long long c0 = (long long)blockIdx.x * 32;
   float acc = 0.f;
-  if (c < cols) {
-#pragma unroll 8
-    for (int i = w; i < lines; i += 8) acc += src[(long long)i * cols + c];
+  if (c0 + l < cols) {
+#pragma unroll 4
+    for (int i = w; i < lines; i += kSumSlices) acc += src[(long long)i * cols + c0 + l];
   }
   s[w][l] = acc;
   __syncthreads();
-  if (w == 0 && c < cols) {
+  // warp w sums column w over the slices
+  acc = s[l][w];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += s[i][l];
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  const long long c = c0 + w;
+  if (l == 0 && c < cols) {
     if (c < split) {
       if (dst0) dst0[c] = acc;
     } else if (dst1) {
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(256) kda_sum_lines_kernel(const float* __restr
 inline cudaError_t launch_sum_lines(const float* src, float* dst0, float* dst1, long long split, int lines,
                                     long long cols, cudaStream_t st) {
   if (cols <= 0) return cudaSuccess;
-  kda_sum_lines_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, st>>>(src, dst0, dst1, split, lines, cols);
+  kda_sum_lines_kernel<<<(unsigned)((cols + 31) / 32), 32 * kSumSlices, 0, st>>>(src, dst0, dst1, split, lines, cols);
   return cudaGetLastError();
 }
 

@@ -8,9 +8,10 @@
 //
 // A row is read once and stays in registers: TPR threads hold it as NV vectors
 // each of VEC elements (16 bytes), strided so that neighbouring threads hold
-// neighbouring vectors.  Rows of up to 32 vectors a lane group take part of a
-// warp (several rows a warp), longer ones a whole CTA.  Sums are fp32.
-// HBM-bound: the traffic is the inputs once and the outputs once.
+// neighbouring vectors.  Rows of up to 32 vectors take part of a warp, and a
+// thread then takes RU rows at once, so that their loads and exchanges overlap;
+// longer ones take a CTA.  Sums are fp32.  HBM-bound: the traffic is the inputs
+// once and the outputs once.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -38,25 +39,36 @@ struct FwdArgs {
   float eps;
 };
 
-// Sum (or maximum) over the TPR threads of a row; every thread gets it.
-template <int TPR, bool kMax>
-__device__ __forceinline__ float row_reduce(float v, float* smem) {
+// Sum (or maximum) of NVAL values each over the TPR threads of a row; every
+// thread gets them.  Rows of several warps go through `smem` (a line of 32 a
+// value); one barrier, so two lots of smem take turns.
+template <int TPR, bool kMax, int NVAL>
+__device__ __forceinline__ void row_reduce(float (&v)[NVAL], float (*smem)[32]) {
   constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = kMax ? max_nan(v, u) : v + u;
-  }
+  for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NVAL; ++i) {
+      const float u = __shfl_xor_sync(0xffffffffu, v[i], o);
+      v[i] = kMax ? max_nan(v[i], u) : v[i] + u;
+    }
   if constexpr (TPR > 32) {
     constexpr int NW = TPR / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) smem[warp] = v;
-    __syncthreads();
-    v = smem[0];
+    if (lane == 0)
 #pragma unroll
-    for (int i = 1; i < NW; ++i) v = kMax ? max_nan(v, smem[i]) : v + smem[i];
+      for (int i = 0; i < NVAL; ++i) smem[i][warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NVAL; ++i) v[i] = smem[i][lane % NW];
+#pragma unroll
+    for (int o = NW / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < NVAL; ++i) {
+        const float u = __shfl_xor_sync(0xffffffffu, v[i], o);
+        v[i] = kMax ? max_nan(v[i], u) : v[i] + u;
+      }
   }
-  return v;
 }
 
 template <int VEC>
@@ -77,111 +89,138 @@ __device__ __forceinline__ void store_fp8(uint8_t* p, const float (&v)[VEC]) {
   }
 }
 
-template <typename T, int VEC, int TPR, int NV, int QUANT>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) kda_rms_norm_fwd_kernel(const FwdArgs a) {
-  constexpr int NT = TPR < 128 ? 128 : TPR;
-  constexpr int RPC = NT / TPR;  // rows a CTA
-  __shared__ float s_red[2][32];
-  const int j = threadIdx.x % TPR;
-  const long long row0 = (long long)blockIdx.x * RPC + threadIdx.x / TPR;
-  const bool live = row0 < a.rows;
-  const long long row = live ? row0 : a.rows - 1;
-  const int nvec = a.D / VEC;
-  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-  const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.D : nullptr;
+constexpr int threads_of(int tpr) { return tpr <= 32 ? 128 : tpr; }  // a row of several warps has its CTA to itself
+// Rows a thread takes at once: a row of one vector is too little work to cover
+// its own loads and exchanges.
+constexpr int rows_at_once(int tpr, int nv) { return tpr <= 32 ? (nv == 1 ? 4 : nv == 2 ? 2 : 1) : 1; }
 
-  float v[NV][VEC];
-  float acc = 0.f;
+template <typename T, int VEC, int TPR, int NV, int QUANT>
+__global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const FwdArgs a) {
+  constexpr int NT = threads_of(TPR);
+  constexpr int RPC = NT / TPR;  // row slots of a CTA
+  constexpr int RU = rows_at_once(TPR, NV);
+  __shared__ float s_red[2][RU][32];
+  const int j = threadIdx.x % TPR;
+  const long long row0 = ((long long)blockIdx.x * RPC + threadIdx.x / TPR) * RU;
+  const int nvec = a.D / VEC;
+  const T* xp = static_cast<const T*>(a.x);
+  const T* rp = static_cast<const T*>(a.residual);
+
+  Pack<T, VEC> px[RU][NV], pr[RU][NV];
+  float v[RU][NV][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = j + i * TPR;
-    if (c < nvec) load_f32<T, VEC>(x + (long long)c * VEC, v[i]);
-    else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-    }
-  }
-  if (res) {
+  for (int u = 0; u < RU; ++u) {
+    const long long row = row0 + u < a.rows ? row0 + u : a.rows - 1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = j + i * TPR;
       if (c < nvec) {
-        float u[VEC];
-        load_f32<T, VEC>(res + (long long)c * VEC, u);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] += u[e];
+        px[u][i] = load_pack<T, VEC>(xp + row * a.x_stride + (long long)c * VEC);
+        if (rp) pr[u][i] = load_pack<T, VEC>(rp + row * a.D + (long long)c * VEC);
       }
     }
   }
+  float w[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
+    if (j + i * TPR < nvec) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, w[i]);
+  float acc[RU];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc = fmaf(v[i][e], v[i][e], acc);
-  // the sum is taken of the unrounded s (the stored s is rounded once, to T)
-  const float r = rsqrtf(row_reduce<TPR, false>(acc, s_red[0]) / (float)a.D + a.eps);
-  if (a.s && live) {
-    T* s = static_cast<T*>(a.s) + row * a.D;
+  for (int u = 0; u < RU; ++u) {
+    acc[u] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = j + i * TPR;
-      if (c < nvec) store_pack<T, VEC>(s + (long long)c * VEC, v[i]);
+      if (j + i * TPR < nvec) {
+        unpack<T, VEC>(px[u][i], v[u][i]);
+        if (rp) {
+          float q[VEC];
+          unpack<T, VEC>(pr[u][i], q);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[u][i][e] += q[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[u][i][e] = w[i][e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[u] = fmaf(v[u][i][e], v[u][i][e], acc[u]);
     }
   }
-  float amax = 0.f;
+  if (a.s) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = j + i * TPR;
-    if (c < nvec) {
-      float w[VEC];
-      load_param<VEC>(a.weight, a.w_bf16, (long long)c * VEC, w);
+    for (int u = 0; u < RU; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = j + i * TPR;
+        if (row0 + u < a.rows && c < nvec)
+          store_pack<T, VEC>(static_cast<T*>(a.s) + (row0 + u) * a.D + (long long)c * VEC, v[u][i]);
+      }
+  }
+  // the sum is taken of the unrounded s (the stored s is rounded once, to T)
+  row_reduce<TPR, false>(acc, s_red[0]);
+  float amax[RU];
+#pragma unroll
+  for (int u = 0; u < RU; ++u) {
+    const float r = rsqrtf(__fdividef(acc[u], (float)a.D) + a.eps);
+    amax[u] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        v[i][e] = v[i][e] * r * w[e];
-        if (QUANT == kRow) amax = max_nan(amax, fabsf(v[i][e]));
+        v[u][i][e] = v[u][i][e] * r * w[i][e];
+        if (QUANT == kRow) amax[u] = max_nan(amax[u], fabsf(v[u][i][e]));
       }
-    }
   }
   if constexpr (QUANT == kNone) {
-    if (!live) return;
-    T* y = static_cast<T*>(a.y) + row * a.D;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = j + i * TPR;
-      if (c < nvec) store_pack<T, VEC>(y + (long long)c * VEC, v[i]);
-    }
-  } else {
-    uint8_t* q = static_cast<uint8_t*>(a.y) + row * a.D;
-    if constexpr (QUANT == kRow) {
-      amax = max_nan(row_reduce<TPR, true>(amax, s_red[1]), kScaleFloor);
-      if (live && j == 0) a.scale[row] = amax / kFp8Max;
-    }
-    const int gl = QUANT == kGroup ? a.group / VEC : 1;  // lanes of one group
+    for (int u = 0; u < RU; ++u)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = j + i * TPR;
-      if constexpr (QUANT == kGroup) {
-        amax = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) amax = max_nan(amax, fabsf(v[i][e]));
-        for (int o = gl >> 1; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        amax = max_nan(amax, kScaleFloor);
-        if (live && c < nvec && (c & (gl - 1)) == 0) a.scale[row * (a.D / a.group) + c / gl] = amax / kFp8Max;
+      for (int i = 0; i < NV; ++i) {
+        const int c = j + i * TPR;
+        if (row0 + u < a.rows && c < nvec)
+          store_pack<T, VEC>(static_cast<T*>(a.y) + (row0 + u) * a.D + (long long)c * VEC, v[u][i]);
       }
-      const float inv = kFp8Max / amax;
-      if (live && c < nvec) {
+  } else {
+    if constexpr (QUANT == kRow) row_reduce<TPR, true>(amax, s_red[1]);
+    const int gl = QUANT == kGroup ? a.group / VEC : 1;  // lanes of one group: a power of two, at most 32
+    const int groups = QUANT == kGroup ? a.D / a.group : 1;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] *= inv;
-        store_fp8<VEC>(q + (long long)c * VEC, v[i]);
+    for (int u = 0; u < RU; ++u) {
+      const bool live = row0 + u < a.rows;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = j + i * TPR;
+        float m = amax[u];
+        if constexpr (QUANT == kGroup) {
+          m = 0.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) m = max_nan(m, fabsf(v[u][i][e]));
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1)
+            if (o < gl) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        m = max_nan(m, kScaleFloor);
+        const bool first = QUANT == kGroup ? (c & (gl - 1)) == 0 : c == 0;
+        if (live && c < nvec && first)
+          a.scale[(row0 + u) * groups + (QUANT == kGroup ? c / gl : 0)] = m / kFp8Max;
+        const float inv = kFp8Max / m;
+        if (live && c < nvec) {
+          float q[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) q[e] = v[u][i][e] * inv;
+          store_fp8<VEC>(static_cast<uint8_t*>(a.y) + (row0 + u) * a.D + (long long)c * VEC, q);
+        }
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  Each CTA takes rows in turn (blockIdx, + gridDim, ...) and keeps
-// its threads' columns of dw in registers over all of them; one line of
-// partial sums per row group goes to the workspace and a second kernel adds
-// the lines in order, so the result does not depend on scheduling.
+// Backward.  Each CTA takes rows in turn (blockIdx, + gridDim, ...), loads the
+// next while it works on one, and keeps its threads' columns of dw in registers
+// over all of them; one line of partial sums per CTA goes to the workspace
+// and a second kernel adds the lines in order, so the result does not depend on
+// scheduling.
 // ---------------------------------------------------------------------------
 struct BwdArgs {
   const void *dy, *s, *weight;
@@ -195,121 +234,143 @@ struct BwdArgs {
 };
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) kda_rms_norm_bwd_kernel(const BwdArgs a) {
-  constexpr int NT = TPR < 128 ? 128 : TPR;
+__global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_bwd_kernel(const BwdArgs a) {
+  constexpr int NT = threads_of(TPR);
   constexpr int RPC = NT / TPR;
+  constexpr bool kKeepW = NV * VEC <= 16;  // weights in registers, or read again for each row
+  constexpr bool kAhead = NV * VEC <= 8;   // the next row's loads in registers, or longer rows hide their own
   __shared__ float s_red[2][2][32];
   const int j = threadIdx.x % TPR;
   const int nvec = a.D / VEC;
-  const long long line = (long long)blockIdx.x * RPC + threadIdx.x / TPR;
   const long long step = (long long)gridDim.x * RPC;
-  float dw[NV][VEC];
+  float dw[NV][VEC], w[kKeepW ? NV : 1][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
-  int buf = 0;
-  // every row group of the CTA runs the same number of turns (reductions are CTA-wide or warp-wide)
-  for (long long base = (long long)blockIdx.x * RPC; base < a.rows; base += step, buf ^= 1) {
-    const long long row0 = base + threadIdx.x / TPR;
-    const bool live = row0 < a.rows;
-    const long long row = live ? row0 : a.rows - 1;
-    const T* dy = static_cast<const T*>(a.dy) + row * a.D;
-    const T* s = static_cast<const T*>(a.s) + row * a.D;
-    float g[NV][VEC], v[NV][VEC];
-    float ss = 0.f, gs = 0.f;
+    if (kKeepW && j + i * TPR < nvec) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, w[kKeepW ? i : 0]);
+  }
+  Pack<T, VEC> pg[NV], ps[NV], pd[NV];
+  auto fetch = [&](long long row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = j + i * TPR;
-      if (c < nvec) {
-        load_f32<T, VEC>(dy + (long long)c * VEC, g[i]);
-        load_f32<T, VEC>(s + (long long)c * VEC, v[i]);
+      if (row < a.rows && c < nvec) {
+        pg[i] = load_pack<T, VEC>(static_cast<const T*>(a.dy) + row * a.D + (long long)c * VEC);
+        ps[i] = load_pack<T, VEC>(static_cast<const T*>(a.s) + row * a.D + (long long)c * VEC);
+        if (kAhead && a.ds) pd[i] = load_pack<T, VEC>(static_cast<const T*>(a.ds) + row * a.D + (long long)c * VEC);
+      }
+    }
+  };
+  if (kAhead) fetch((long long)blockIdx.x * RPC + threadIdx.x / TPR);
+  int buf = 0;
+  const float inv_d = 1.f / (float)a.D;
+  // every row slot of the CTA runs the same number of turns (reductions are CTA-wide or warp-wide)
+  for (long long base = (long long)blockIdx.x * RPC; base < a.rows; base += step, buf ^= 1) {
+    const long long row = base + threadIdx.x / TPR;
+    const bool live = row < a.rows;
+    float g[NV][VEC], v[NV][VEC], d[kAhead ? NV : 1][VEC];
+    if (!kAhead) fetch(row);
+    float sums[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = j + i * TPR;
+      if (live && c < nvec) {
+        unpack<T, VEC>(pg[i], g[i]);
+        unpack<T, VEC>(ps[i], v[i]);
+        if (kAhead && a.ds) unpack<T, VEC>(pd[i], d[kAhead ? i : 0]);
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) g[i][e] = v[i][e] = 0.f;
       }
+      if (!a.ds)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) d[kAhead ? i : 0][e] = 0.f;
     }
+    if (kAhead) fetch(row + step);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = j + i * TPR;
-      if (c < nvec) {
-        float w[VEC];
-        load_param<VEC>(a.weight, a.w_bf16, (long long)c * VEC, w);
+      if (j + i * TPR < nvec) {
+        float wv[VEC];
+        if (!kKeepW) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, wv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          ss = fmaf(v[i][e], v[i][e], ss);
-          gs = fmaf(g[i][e] * w[e], v[i][e], gs);
+          const float we = kKeepW ? w[kKeepW ? i : 0][e] : wv[e];
+          sums[0] = fmaf(v[i][e], v[i][e], sums[0]);
+          sums[1] = fmaf(g[i][e] * we, v[i][e], sums[1]);
         }
       }
     }
-    ss = row_reduce<TPR, false>(ss, s_red[buf][0]);
-    gs = row_reduce<TPR, false>(gs, s_red[buf][1]);
-    const float r = rsqrtf(ss / (float)a.D + a.eps);
-    const float k = r * r * r * (gs / (float)a.D);
-    T* dx = static_cast<T*>(a.dx) + row * a.D;
-    const T* ds = a.ds ? static_cast<const T*>(a.ds) + row * a.D : nullptr;
+    row_reduce<TPR, false>(sums, s_red[buf]);
+    const float r = rsqrtf(sums[0] * inv_d + a.eps);
+    const float k = r * r * r * (sums[1] * inv_d);
     if (live) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = j + i * TPR;
         if (c < nvec) {
-          float w[VEC], o[VEC], u[VEC];
-          load_param<VEC>(a.weight, a.w_bf16, (long long)c * VEC, w);
-          if (ds) load_f32<T, VEC>(ds + (long long)c * VEC, u);
+          float wv[VEC], o[VEC];
+          if (!kKeepW) load_param<VEC>(a.weight, a.w_bf16, (long long)c * VEC, wv);
+          if (!kAhead && a.ds)
+            load_f32<T, VEC>(static_cast<const T*>(a.ds) + row * a.D + (long long)c * VEC, d[kAhead ? i : 0]);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
+            const float we = kKeepW ? w[kKeepW ? i : 0][e] : wv[e];
             dw[i][e] = fmaf(g[i][e] * v[i][e], r, dw[i][e]);
-            o[e] = r * w[e] * g[i][e] - k * v[i][e] + (ds ? u[e] : 0.f);
+            o[e] = fmaf(r * we, g[i][e], fmaf(-k, v[i][e], d[kAhead ? i : 0][e]));
           }
-          store_pack<T, VEC>(dx + (long long)c * VEC, o);
+          store_pack<T, VEC>(static_cast<T*>(a.dx) + row * a.D + (long long)c * VEC, o);
         }
       }
     }
   }
-  float* p = a.partial + line * a.D;
+  if constexpr (RPC > 1) {  // the row slots of the CTA (rows of one vector a thread), added in order
+    __shared__ __align__(16) float s_dw[RPC][TPR * VEC];
+    store_floats<VEC>(&s_dw[threadIdx.x / TPR][j * VEC], dw[0]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.D; c += NT) {
+      float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = j + i * TPR;
-    if (c < nvec) {
+      for (int i = 0; i < RPC; ++i) sum += s_dw[i][c];
+      a.partial[(long long)blockIdx.x * a.D + c] = sum;
+    }
+  } else {
+    float* p = a.partial + (long long)blockIdx.x * a.D;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) p[(long long)c * VEC + e] = dw[i][e];
+    for (int i = 0; i < NV; ++i) {
+      const int c = j + i * TPR;
+      if (c < nvec) store_floats<VEC>(p + (long long)c * VEC, dw[i]);
     }
   }
 }
 
-// Host: the row shapes built, smallest first.  `vecs` vectors a row.
+// Host: the row shapes built, smallest first.  `vecs` vectors a row: a vector a
+// thread as long as that gives a CTA of at most 512 threads.
 struct RowShape {
   int tpr, nv;
 };
 inline RowShape row_shape(int vecs) {
-  if (vecs <= 8) return {8, 1};
-  if (vecs <= 16) return {16, 1};
-  if (vecs <= 32) return {32, 1};
-  if (vecs <= 64) return {32, 2};
-  if (vecs <= 128) return {32, 4};
-  if (vecs <= 256) return {128, 2};
-  if (vecs <= 512) return {128, 4};
-  if (vecs <= 1024) return {256, 4};
-  if (vecs <= 2048) return {512, 4};
-  if (vecs <= 4096) return {512, 8};
-  if (vecs <= 8192) return {512, 16};
+  for (int tpr = 8; tpr <= 512; tpr *= 2)
+    if (vecs <= tpr) return {tpr, 1};
+  for (int nv : {2, 3, 4, 8, 16})
+    if (vecs <= 512 * nv) return {512, nv};
   return {512, 32};
 }
 
 #define KDA_NORM_SHAPES(CASE) \
-  CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(32, 2) CASE(32, 4) CASE(128, 2) CASE(128, 4) CASE(256, 4) CASE(512, 4)
+  CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(64, 1) CASE(128, 1) CASE(256, 1) CASE(512, 1) CASE(512, 2) CASE(512, 3) \
+  CASE(512, 4)
 #define KDA_NORM_SHAPES_LONG(CASE) CASE(512, 8)
 #define KDA_NORM_SHAPES_SCALAR(CASE) CASE(512, 16) CASE(512, 32)
 
 template <typename T, int VEC, int QUANT>
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t st) {
   const RowShape sh = row_shape(a.D / VEC);
-#define KDA_CASE(TPR, NV)                                                                             \
-  if (sh.tpr == TPR && sh.nv == NV) {                                                                  \
-    constexpr int NT = TPR < 128 ? 128 : TPR;                                                           \
-    const long long grid = (a.rows + NT / TPR - 1) / (NT / TPR);                                        \
-    kda_rms_norm_fwd_kernel<T, VEC, TPR, NV, QUANT><<<(unsigned)grid, NT, 0, st>>>(a);                  \
-    return cudaGetLastError();                                                                          \
+#define KDA_CASE(TPR, NV)                                                                               \
+  if (sh.tpr == TPR && sh.nv == NV) {                                                                    \
+    constexpr int NT = threads_of(TPR), RPC = NT / TPR * rows_at_once(TPR, NV);                           \
+    kda_rms_norm_fwd_kernel<T, VEC, TPR, NV, QUANT><<<(unsigned)((a.rows + RPC - 1) / RPC), NT, 0, st>>>(a); \
+    return cudaGetLastError();                                                                            \
   }
   KDA_NORM_SHAPES(KDA_CASE)
   if constexpr (VEC < 8) { KDA_NORM_SHAPES_LONG(KDA_CASE) }
@@ -318,33 +379,31 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t st) {
   return cudaErrorInvalidValue;
 }
 
-// Lines of partial sums of the backward: one per row group of each CTA.
-struct BwdPlan {
-  int grid, rpc;
-};
-inline BwdPlan bwd_plan(long long rows, int vecs) {
+// Lines of partial sums of the backward: one per CTA, as many CTAs as run at
+// once (about 1024 threads an SM).
+inline int bwd_grid(long long rows, int vecs) {
   const RowShape sh = row_shape(vecs);
-  const int nt = sh.tpr < 128 ? 128 : sh.tpr, rpc = nt / sh.tpr;
+  const int nt = threads_of(sh.tpr), rpc = nt / sh.tpr;
   const long long want = (rows + rpc - 1) / rpc, most = 148LL * (1024 / nt);
-  return {(int)(want < most ? want : most), rpc};
+  return (int)(want < most ? want : most);
 }
 
 template <typename T, int VEC>
 cudaError_t launch_bwd(const BwdArgs& a, float* dweight, cudaStream_t st) {
   const RowShape sh = row_shape(a.D / VEC);
-  const BwdPlan plan = bwd_plan(a.rows, a.D / VEC);
+  const int grid = bwd_grid(a.rows, a.D / VEC);
   cudaError_t e = cudaErrorInvalidValue;
-#define KDA_CASE(TPR, NV)                                                                             \
-  if (sh.tpr == TPR && sh.nv == NV) {                                                                  \
-    kda_rms_norm_bwd_kernel<T, VEC, TPR, NV><<<plan.grid, TPR < 128 ? 128 : TPR, 0, st>>>(a);            \
-    e = cudaGetLastError();                                                                             \
+#define KDA_CASE(TPR, NV)                                                                          \
+  if (sh.tpr == TPR && sh.nv == NV) {                                                               \
+    kda_rms_norm_bwd_kernel<T, VEC, TPR, NV><<<grid, threads_of(TPR), 0, st>>>(a);              \
+    e = cudaGetLastError();                                                                          \
   }
   KDA_NORM_SHAPES(KDA_CASE)
   if constexpr (VEC < 8) { KDA_NORM_SHAPES_LONG(KDA_CASE) }
   if constexpr (VEC == 1) { KDA_NORM_SHAPES_SCALAR(KDA_CASE) }
 #undef KDA_CASE
   if (e != cudaSuccess) return e;
-  return launch_sum_lines(a.partial, dweight, nullptr, a.D, plan.grid * plan.rpc, a.D, st);
+  return launch_sum_lines(a.partial, dweight, nullptr, a.D, grid, a.D, st);
 }
 
 }  // namespace norm

@@ -186,9 +186,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
           const float2 dl = dup2(s.delta[t][ch]), u = dup2(s.u[t][ch]), gy = dup2(s.dyy[t][ch]);
           const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
           const float4 c4 = *reinterpret_cast<const float4*>(&s.C[t][sl * 4]);
-          const float2 e0 = mul2(dl, A2[0]), e1 = mul2(dl, A2[1]);
-          da[k][0] = make_float2(ex2(e0.x), ex2(e0.y));
-          da[k][1] = make_float2(ex2(e1.x), ex2(e1.y));
+          da[k][0] = decay2(dl, A2[0]);
+          da[k][1] = decay2(dl, A2[1]);
           if (s.first[t] >= 0) {
             h0 = h1 = dup2(0.f);
             if (a.S0) {
