@@ -117,7 +117,7 @@ kda_status_t norm_fwd_impl(const char* fn, int quant, const void* x, long long x
                     aligned(weight, weight_dtype == KDA_F32 ? 16u : 2u * vec);
   if (quant == kda::norm::kGroup && !wide)
     return misaligned(fn, "group scales need 16-byte aligned rows and pointers");
-  kda::norm::FwdArgs a{x, x_stride, residual, weight, weight_dtype == KDA_BF16, y, scale, s, rows, D, group, eps};
+  kda::norm::FwdArgs a{x, x_stride, residual, weight, weight_dtype == KDA_BF16, y, scale, s, rows, D, group, eps, 0, 1};
   cudaError_t e = cudaErrorInvalidValue;
 #define KDA_NORM_CASE(TYPE, V)                                                                        \
   e = quant == kda::norm::kNone  ? kda::norm::launch_fwd<TYPE, V, kda::norm::kNone>(a, stream)         \

@@ -122,6 +122,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+// One element kept in a 32-bit register as it was loaded (two 16-bit values
+// packed into one register would have to arrive before the packing, which ends
+// the overlap of a load issued ahead).
+template <typename T>
+__device__ __forceinline__ uint32_t load_raw(const T* p);
+template <>
+__device__ __forceinline__ uint32_t load_raw<float>(const float* p) { return __float_as_uint(*p); }
+template <>
+__device__ __forceinline__ uint32_t load_raw<__nv_bfloat16>(const __nv_bfloat16* p) {
+  return *reinterpret_cast<const unsigned short*>(p);
+}
+template <typename T>
+__device__ __forceinline__ float raw_to_f32(uint32_t r) {
+  return sizeof(T) == 2 ? __uint_as_float(r << 16) : __uint_as_float(r);
+}
+
 // Two fp32 lanes in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;

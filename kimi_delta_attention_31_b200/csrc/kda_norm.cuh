@@ -9,7 +9,7 @@
 // A row is read once and stays in registers: TPR threads hold it as NV vectors
 // each of VEC elements (16 bytes), strided so that neighbouring threads hold
 // neighbouring vectors.  Rows of up to 32 vectors take part of a warp, and a
-// thread then takes RU rows at once, so that their loads and exchanges overlap;
+// thread then takes RU = 2 rows at once, so that their loads and exchanges overlap;
 // longer ones take a CTA.  Sums are fp32.  HBM-bound: the traffic is the inputs
 // once and the outputs once.
 #pragma once
@@ -37,6 +37,7 @@ struct FwdArgs {
   long long rows;
   int D, group;
   float eps;
+  int group_lanes_log2, groups;  // kGroup: lanes of one group (2^.., at most 32), groups a row
 };
 
 // Sum (or maximum) of NVAL values each over the TPR threads of a row; every
@@ -92,10 +93,10 @@ __device__ __forceinline__ void store_fp8(uint8_t* p, const float (&v)[VEC]) {
 constexpr int threads_of(int tpr) { return tpr <= 32 ? 128 : tpr; }  // a row of several warps has its CTA to itself
 // Rows a thread takes at once: a row of one vector is too little work to cover
 // its own loads and exchanges.
-constexpr int rows_at_once(int tpr, int nv) { return tpr <= 32 ? (nv == 1 ? 4 : nv == 2 ? 2 : 1) : 1; }
+constexpr int rows_at_once(int tpr, int nv) { return tpr <= 32 && nv == 1 ? 2 : 1; }
 
 template <typename T, int VEC, int TPR, int NV, int QUANT>
-__global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 ? 8 : 1) kda_rms_norm_fwd_kernel(const FwdArgs a) {
   constexpr int NT = threads_of(TPR);
   constexpr int RPC = NT / TPR;  // row slots of a CTA
   constexpr int RU = rows_at_once(TPR, NV);
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
   for (int i = 0; i < NV; ++i)
     if (j + i * TPR < nvec) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, w[i]);
   float acc[RU];
+  const float inv_d = 1.f / (float)a.D;
 #pragma unroll
   for (int u = 0; u < RU; ++u) {
     acc[u] = 0.f;
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
   float amax[RU];
 #pragma unroll
   for (int u = 0; u < RU; ++u) {
-    const float r = rsqrtf(__fdividef(acc[u], (float)a.D) + a.eps);
+    const float r = rsqrtf(acc[u] * inv_d + a.eps);
     amax[u] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -182,8 +184,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
       }
   } else {
     if constexpr (QUANT == kRow) row_reduce<TPR, true>(amax, s_red[1]);
-    const int gl = QUANT == kGroup ? a.group / VEC : 1;  // lanes of one group: a power of two, at most 32
-    const int groups = QUANT == kGroup ? a.D / a.group : 1;
+    const int gl = 1 << a.group_lanes_log2;
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       const bool live = row0 + u < a.rows;
@@ -202,8 +203,9 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
         m = max_nan(m, kScaleFloor);
         const bool first = QUANT == kGroup ? (c & (gl - 1)) == 0 : c == 0;
         if (live && c < nvec && first)
-          a.scale[(row0 + u) * groups + (QUANT == kGroup ? c / gl : 0)] = m / kFp8Max;
-        const float inv = kFp8Max / m;
+          a.scale[(row0 + u) * a.groups + (QUANT == kGroup ? c >> a.group_lanes_log2 : 0)] = m / kFp8Max;
+        // 448 / m: the reciprocal's argument scaled down, so that a huge m does not flush it to 0
+        const float inv = fast_rcp(m * 0x1p-10f) * (kFp8Max * 0x1p-10f);
         if (live && c < nvec) {
           float q[VEC];
 #pragma unroll
@@ -234,11 +236,11 @@ struct BwdArgs {
 };
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / threads_of(TPR) : 1) kda_rms_norm_bwd_kernel(const BwdArgs a) {
   constexpr int NT = threads_of(TPR);
   constexpr int RPC = NT / TPR;
   constexpr bool kKeepW = NV * VEC <= 16;  // weights in registers, or read again for each row
-  constexpr bool kAhead = NV * VEC <= 8;   // the next row's loads in registers, or longer rows hide their own
+  constexpr bool kAhead = NV * VEC <= 16;   // the next row's loads in registers, or longer rows hide their own
   __shared__ float s_red[2][2][32];
   const int j = threadIdx.x % TPR;
   const int nvec = a.D / VEC;
@@ -269,7 +271,8 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_bwd_kernel(const
   for (long long base = (long long)blockIdx.x * RPC; base < a.rows; base += step, buf ^= 1) {
     const long long row = base + threadIdx.x / TPR;
     const bool live = row < a.rows;
-    float g[NV][VEC], v[NV][VEC], d[kAhead ? NV : 1][VEC];
+    float g[NV][VEC], v[NV][VEC];
+    Pack<T, VEC> d[kAhead ? NV : 1];
     if (!kAhead) fetch(row);
     float sums[2] = {0.f, 0.f};
 #pragma unroll
@@ -278,14 +281,11 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_bwd_kernel(const
       if (live && c < nvec) {
         unpack<T, VEC>(pg[i], g[i]);
         unpack<T, VEC>(ps[i], v[i]);
-        if (kAhead && a.ds) unpack<T, VEC>(pd[i], d[kAhead ? i : 0]);
+        if (kAhead && a.ds) d[kAhead ? i : 0] = pd[i];
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) g[i][e] = v[i][e] = 0.f;
       }
-      if (!a.ds)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) d[kAhead ? i : 0][e] = 0.f;
     }
     if (kAhead) fetch(row + step);
 #pragma unroll
@@ -311,22 +311,25 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_bwd_kernel(const
         if (c < nvec) {
           float wv[VEC], o[VEC];
           if (!kKeepW) load_param<VEC>(a.weight, a.w_bf16, (long long)c * VEC, wv);
-          if (!kAhead && a.ds)
-            load_f32<T, VEC>(static_cast<const T*>(a.ds) + row * a.D + (long long)c * VEC, d[kAhead ? i : 0]);
+          float de[VEC] = {};
+          if (a.ds)
+            unpack<T, VEC>(kAhead ? d[kAhead ? i : 0]
+                                  : load_pack<T, VEC>(static_cast<const T*>(a.ds) + row * a.D + (long long)c * VEC), de);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
             const float we = kKeepW ? w[kKeepW ? i : 0][e] : wv[e];
             dw[i][e] = fmaf(g[i][e] * v[i][e], r, dw[i][e]);
-            o[e] = fmaf(r * we, g[i][e], fmaf(-k, v[i][e], d[kAhead ? i : 0][e]));
+            o[e] = fmaf(r * we, g[i][e], fmaf(-k, v[i][e], de[e]));
           }
           store_pack<T, VEC>(static_cast<T*>(a.dx) + row * a.D + (long long)c * VEC, o);
         }
       }
     }
   }
-  if constexpr (RPC > 1) {  // the row slots of the CTA (rows of one vector a thread), added in order
-    __shared__ __align__(16) float s_dw[RPC][TPR * VEC];
-    store_floats<VEC>(&s_dw[threadIdx.x / TPR][j * VEC], dw[0]);
+  if constexpr (RPC > 1) {  // the row slots of the CTA, added in order
+    __shared__ __align__(16) float s_dw[RPC][TPR * VEC * NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) store_floats<VEC>(&s_dw[threadIdx.x / TPR][(j + i * TPR) * VEC], dw[i]);
     __syncthreads();
     for (int c = threadIdx.x; c < a.D; c += NT) {
       float sum = 0.f;
@@ -357,15 +360,29 @@ inline RowShape row_shape(int vecs) {
   return {512, 32};
 }
 
+// Backward: two vectors a thread where a row takes several warps, which halves
+// the exchanges and keeps enough loads in flight.
+inline RowShape row_shape_bwd(int vecs) {
+  const RowShape f = row_shape(vecs);
+  return f.tpr > 32 && f.nv == 1 ? RowShape{f.tpr / 2, 2} : f;
+}
+
 #define KDA_NORM_SHAPES(CASE) \
   CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(64, 1) CASE(128, 1) CASE(256, 1) CASE(512, 1) CASE(512, 2) CASE(512, 3) \
+  CASE(512, 4)
+#define KDA_NORM_SHAPES_BWD(CASE) \
+  CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(32, 2) CASE(64, 2) CASE(128, 2) CASE(256, 2) CASE(512, 2) CASE(512, 3) \
   CASE(512, 4)
 #define KDA_NORM_SHAPES_LONG(CASE) CASE(512, 8)
 #define KDA_NORM_SHAPES_SCALAR(CASE) CASE(512, 16) CASE(512, 32)
 
 template <typename T, int VEC, int QUANT>
-cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t st) {
+cudaError_t launch_fwd(FwdArgs a, cudaStream_t st) {
   const RowShape sh = row_shape(a.D / VEC);
+  a.group_lanes_log2 = 0;
+  a.groups = QUANT == kGroup ? a.D / a.group : 1;
+  if (QUANT == kGroup)
+    while ((VEC << a.group_lanes_log2) < a.group) ++a.group_lanes_log2;
 #define KDA_CASE(TPR, NV)                                                                               \
   if (sh.tpr == TPR && sh.nv == NV) {                                                                    \
     constexpr int NT = threads_of(TPR), RPC = NT / TPR * rows_at_once(TPR, NV);                           \
@@ -380,17 +397,17 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t st) {
 }
 
 // Lines of partial sums of the backward: one per CTA, as many CTAs as run at
-// once (about 1024 threads an SM).
+// once (512 threads an SM).
 inline int bwd_grid(long long rows, int vecs) {
-  const RowShape sh = row_shape(vecs);
+  const RowShape sh = row_shape_bwd(vecs);
   const int nt = threads_of(sh.tpr), rpc = nt / sh.tpr;
-  const long long want = (rows + rpc - 1) / rpc, most = 148LL * (1024 / nt);
+  const long long want = (rows + rpc - 1) / rpc, most = 148LL * (512 / nt);
   return (int)(want < most ? want : most);
 }
 
 template <typename T, int VEC>
 cudaError_t launch_bwd(const BwdArgs& a, float* dweight, cudaStream_t st) {
-  const RowShape sh = row_shape(a.D / VEC);
+  const RowShape sh = row_shape_bwd(a.D / VEC);
   const int grid = bwd_grid(a.rows, a.D / VEC);
   cudaError_t e = cudaErrorInvalidValue;
 #define KDA_CASE(TPR, NV)                                                                          \
@@ -398,7 +415,7 @@ cudaError_t launch_bwd(const BwdArgs& a, float* dweight, cudaStream_t st) {
     kda_rms_norm_bwd_kernel<T, VEC, TPR, NV><<<grid, threads_of(TPR), 0, st>>>(a);              \
     e = cudaGetLastError();                                                                          \
   }
-  KDA_NORM_SHAPES(KDA_CASE)
+  KDA_NORM_SHAPES_BWD(KDA_CASE)
   if constexpr (VEC < 8) { KDA_NORM_SHAPES_LONG(KDA_CASE) }
   if constexpr (VEC == 1) { KDA_NORM_SHAPES_SCALAR(KDA_CASE) }
 #undef KDA_CASE

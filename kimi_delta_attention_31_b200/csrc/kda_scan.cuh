@@ -52,10 +52,26 @@ struct Shape {
   static constexpr int CH = kThreads / LPC;     // channels a CTA
 };
 
-// log(1 + e^v), to fp32 accuracy also where it is small.
-__device__ __forceinline__ float softplus_f(float v) {
-  return fmaxf(v, 0.f) + log1pf(ex2(-fabsf(v) * kLog2eF));
+// log(1 + e^v) of two values, to fp32 accuracy also where it is small:
+// max(v, 0) + log1p(e), e = e^-|v| in (0, 1], with log1p(e) / e by its minimax
+// polynomial of degree 9 on [0, 1] (relative error 5e-9, fitted by Lawson's
+// iteration).
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2eF), ex2(-fabsf(v.y) * kLog2eF));
+  float2 q = dup2(-0.0032440247014164925f);
+  q = fma2(q, e, dup2(0.019851461052894592f));
+  q = fma2(q, e, dup2(-0.05695953220129013f));
+  q = fma2(q, e, dup2(0.10603654384613037f));
+  q = fma2(q, e, dup2(-0.15305592119693756f));
+  q = fma2(q, e, dup2(0.1967593878507614f));
+  q = fma2(q, e, dup2(-0.24954134225845337f));
+  q = fma2(q, e, dup2(0.3332996368408203f));
+  q = fma2(q, e, dup2(-0.4999990165233612f));
+  q = fma2(q, e, dup2(1.f));
+  // max that keeps NaN: a NaN time step makes its channel NaN
+  return fma2(q, e, make_float2(max_nan(v.x, 0.f), max_nan(v.y, 0.f)));
 }
+__device__ __forceinline__ float softplus_f(float v) { return softplus2(dup2(v)).x; }
 
 // exp(delta A) from A2 = A log2(e).  The hardware's ex2 lies low, by 0.3 to 0.8
 // units of 2^-24 on average over exponents of -4 to -0.0005, and a state of
@@ -98,8 +114,14 @@ enum Mode : int { kForward = 0, kLocal = 1, kLocalBwd = 2 };
 //   before it, with nothing coming from its right:
 //     sum_t (prod_{s <= t} a_s) C_t dyy_t,  dyy = dy silu(z), up to the first
 //   sequence start in the chunk.
+//
+// A tile of kTile tokens inside one sequence runs without a branch, so that the
+// exponentials of later tokens cover the chains of earlier ones, on inputs
+// loaded a tile ahead; a tile in which a sequence ends, or a last one that is
+// not full, goes token by token.
 template <typename T, int S, int MODE>
-__global__ void __launch_bounds__(kThreads) kda_selective_scan_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, MODE == kLocal ? 4 : MODE == kForward ? 3 : 2)
+    kda_selective_scan_kernel(const Args a) {
   using Sh = Shape<S>;
   constexpr int SPT = Sh::SPT, LPC = Sh::LPC, NP = SPT / 2;
   constexpr bool kC = MODE != kLocal, kZ = MODE != kLocal;
@@ -136,6 +158,7 @@ __global__ void __launch_bounds__(kThreads) kda_selective_scan_kernel(const Args
   for (int i = 0; i < NP; ++i) A2[i] = mul2(A2[i], dup2(kLog2eF));
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
   const float Dc = kC && a.Dv ? a.Dv[c] : 0.f;
+  const bool gated = kZ && a.z;
 
   int n = seq_of_token(a.q, t0);
   long long end = seq_end(a.q, n);
@@ -143,129 +166,170 @@ __global__ void __launch_bounds__(kThreads) kda_selective_scan_kernel(const Args
   if (cut && a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
   else if (!cut && MODE == kForward && a.entry) load_state<NP>(a.entry + chunk * a.d * S + crow, h);
   else zero_state<NP>(h);
-  float2 P[NP], R[NP];  // kLocalBwd: product of the decays so far, gradient sent to the left
-  if (MODE == kLocalBwd) {
+  constexpr int NPB = MODE == kLocalBwd ? NP : 1;
+  float2 P[NPB], R[NPB];  // kLocalBwd: product of the decays so far, gradient sent to the left
 #pragma unroll
-    for (int i = 0; i < NP; ++i) P[i] = dup2(cut ? 0.f : 1.f), R[i] = dup2(0.f);
-  }
+  for (int i = 0; i < NPB; ++i) P[i] = dup2(cut ? 0.f : 1.f), R[i] = dup2(0.f);
   float sumd = 0.f;
 
-  const T* xp = static_cast<const T*>(a.x) + c;
-  const T* dtp = static_cast<const T*>(a.dt) + c;
-  const T* zp = static_cast<const T*>(a.z) + c;
-  const T* dyp = static_cast<const T*>(a.dy) + c;
-  const T* Bp = static_cast<const T*>(a.B) + (long long)grp * S;
-  const T* Cp = static_cast<const T*>(a.C) + (long long)grp * S;
+  const T* xp = static_cast<const T*>(a.x) + t0 * a.xs + c;
+  const T* dtp = static_cast<const T*>(a.dt) + t0 * a.dts + c;
+  const T* zp = gated ? static_cast<const T*>(a.z) + t0 * a.zs + c : nullptr;
+  const T* dyp = MODE == kLocalBwd ? static_cast<const T*>(a.dy) + t0 * a.d + c : nullptr;
+  T* yp = MODE == kForward ? static_cast<T*>(a.y) + t0 * a.d + c : nullptr;
 
-  T rx[kTile], rdt[kTile], rz[kTile], rdy[kTile], rB[NBC], rC[NBC];
-  auto fetch = [&](long long t) {
+  uint32_t rx[kTile], rdt[kTile], rz[kTile], rdy[MODE == kLocalBwd ? kTile : 1], rB[NBC], rC[NBC];
+  auto fetch_bc = [&](long long t) {  // tokens past the chunk repeat its last one and are not used
 #pragma unroll
     for (int i = 0; i < NBC; ++i) {
       const int e = i * kThreads + (int)threadIdx.x;
       const long long tt = t + e / S < t1 ? t + e / S : t1 - 1;
       if (e < kTile * S) {
-        rB[i] = Bp[tt * a.bs + e % S];
-        if (kC) rC[i] = Cp[tt * a.cs + e % S];
+        rB[i] = load_raw<T>(static_cast<const T*>(a.B) + tt * a.bs + (long long)grp * S + e % S);
+        if (kC) rC[i] = load_raw<T>(static_cast<const T*>(a.C) + tt * a.cs + (long long)grp * S + e % S);
       }
     }
+  };
+  auto fetch = [&](const T* px, const T* pdt, const T* pz, const T* pdy) {
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
-      const long long tt = t + i < t1 ? t + i : t1 - 1;
-      rx[i] = xp[tt * a.xs];
-      rdt[i] = dtp[tt * a.dts];
-      if (kZ && a.z) rz[i] = zp[tt * a.zs];
-      if (MODE == kLocalBwd) rdy[i] = dyp[tt * a.d];
+      rx[i] = load_raw<T>(px + i * a.xs);
+      rdt[i] = load_raw<T>(pdt + i * a.dts);
+      if (gated) rz[i] = load_raw<T>(pz + i * a.zs);
+      if (MODE == kLocalBwd) rdy[i] = load_raw<T>(pdy + (long long)i * a.d);
     }
   };
-  fetch(t0);
+  // one token: gv is the gate (kForward) or dy times it (kLocalBwd); last: with the final state's gradient
+  auto token = [&](float delta, float xv, float gv, const float* tb, const float* tc, bool last) -> float {
+    const float2 dd = dup2(delta), uu = dup2(delta * xv);
+    float2 acc = dup2(0.f), acc1 = dup2(0.f);
+#pragma unroll
+    for (int p = 0; p < NP; p += 2) {
+      const float4 b4 = *reinterpret_cast<const float4*>(tb + sl * SPT + 2 * p);
+      const float2 w0 = decay2(dd, A2[p]), w1 = decay2(dd, A2[p + 1]);
+      h[p] = fma2(w0, h[p], mul2(uu, make_float2(b4.x, b4.y)));
+      h[p + 1] = fma2(w1, h[p + 1], mul2(uu, make_float2(b4.z, b4.w)));
+      if constexpr (kC) {
+        const float4 c4 = *reinterpret_cast<const float4*>(tc + sl * SPT + 2 * p);
+        if constexpr (MODE == kForward) {
+          acc = fma2(h[p], make_float2(c4.x, c4.y), acc);
+          acc1 = fma2(h[p + 1], make_float2(c4.z, c4.w), acc1);
+        } else {
+          P[p] = mul2(P[p], w0);
+          P[p + 1] = mul2(P[p + 1], w1);
+          float2 g0 = mul2(dup2(gv), make_float2(c4.x, c4.y)), g1 = mul2(dup2(gv), make_float2(c4.z, c4.w));
+          if (last) {
+            const float4 s4 = *reinterpret_cast<const float4*>(a.dS + (long long)n * a.d * S + crow + 2 * p);
+            g0 = add2(g0, make_float2(s4.x, s4.y));
+            g1 = add2(g1, make_float2(s4.z, s4.w));
+          }
+          R[p] = fma2(P[p], g0, R[p]);
+          R[p + 1] = fma2(P[p + 1], g1, R[p + 1]);
+        }
+      }
+    }
+    if (MODE != kForward) return 0.f;
+    acc = add2(acc, acc1);
+    float yy = acc.x + acc.y;
+#pragma unroll
+    for (int o = LPC / 2; o > 0; o >>= 1) yy += __shfl_xor_sync(0xffffffffu, yy, o);
+    return fmaf(Dc, xv, yy) * gv;
+  };
+
+  fetch_bc(t0);
+  if (t0 + kTile <= t1) fetch(xp, dtp, zp, dyp);
   int buf = 0;
   for (long long t = t0; t < t1; t += kTile, buf ^= 1) {
 #pragma unroll
     for (int i = 0; i < NBC; ++i) {
       const int e = i * kThreads + (int)threadIdx.x;
       if (e < kTile * S) {
-        (&sB[buf][0][0])[e] = to_f32<T>(rB[i]);
-        if (kC) (&sC[kC ? buf : 0][0][0])[e] = to_f32<T>(rC[i]);
+        (&sB[buf][0][0])[e] = raw_to_f32<T>(rB[i]);
+        if (kC) (&sC[kC ? buf : 0][0][0])[e] = raw_to_f32<T>(rC[i]);
       }
     }
     __syncthreads();  // the other buffer is free: its readers passed this point a tile ago
-    float xv[kTile], dv[kTile], gv[kTile], yv[kTile];
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      xv[i] = to_f32<T>(rx[i]);
-      dv[i] = softplus_f(to_f32<T>(rdt[i]) + bias);
-      if (kZ) {
-        const float zz = a.z ? to_f32<T>(rz[i]) : 0.f;
-        gv[i] = a.z ? zz * fast_sigmoid(zz) : 1.f;
-      }
-      if (MODE == kLocalBwd) gv[i] *= to_f32<T>(rdy[i]);
+    if (t + kTile < t1) fetch_bc(t + kTile);
+    if (t == end) {  // the first token of another sequence
+      if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
+      n = seq_of_token(a.q, t);
+      end = seq_end(a.q, n);
+      cut = true;
+      if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
+      else zero_state<NP>(h);
+      if (MODE == kLocalBwd) zero_state<NPB>(P);
     }
-    if (t + kTile < t1) fetch(t + kTile);
     float part = 0.f;
+    // a final state's gradient is added at its sequence's last token, so that tile goes token by token too
+    if (t + kTile <= t1 && (t >= end || t + kTile + (MODE == kLocalBwd) <= end)) {
+      float xv[kTile], dv[kTile], gv[kTile];
 #pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      const long long ti = t + i;
-      if (ti < t1) {
-        if (ti == end) {  // the first token of another sequence
+      for (int i = 0; i < kTile; i += 2) {
+        const float2 d2 = softplus2(add2(make_float2(raw_to_f32<T>(rdt[i]), raw_to_f32<T>(rdt[i + 1])), dup2(bias)));
+        dv[i] = d2.x;
+        dv[i + 1] = d2.y;
+      }
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) {
+        xv[i] = raw_to_f32<T>(rx[i]);
+        gv[i] = 1.f;
+        if (gated) {
+          const float zz = raw_to_f32<T>(rz[i]);
+          gv[i] = zz * fast_sigmoid(zz);
+        }
+        if (MODE == kLocalBwd) gv[i] *= raw_to_f32<T>(rdy[i]);
+      }
+      if (t + 2 * kTile <= t1)
+        fetch(xp + kTile * a.xs, dtp + kTile * a.dts, gated ? zp + kTile * a.zs : nullptr,
+              MODE == kLocalBwd ? dyp + (long long)kTile * a.d : nullptr);
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) {
+        const float y = token(dv[i], xv[i], gv[i], sB[buf][i], kC ? sC[kC ? buf : 0][kC ? i : 0] : nullptr, false);
+        part += dv[i];
+        if (MODE == kForward && active && sl == 0) yp[(long long)i * a.d] = from_f32<T>(y);
+      }
+    } else {
+      const int m = t1 - t < kTile ? (int)(t1 - t) : kTile;
+#pragma unroll 1
+      for (int i = 0; i < m; ++i) {
+        if (i > 0 && t + i == end) {
           if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
-          n = seq_of_token(a.q, ti);
+          n = seq_of_token(a.q, t + i);
           end = seq_end(a.q, n);
           cut = true;
           if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
           else zero_state<NP>(h);
-          if (MODE == kLocalBwd) zero_state<NP>(P);
+          if (MODE == kLocalBwd) zero_state<NPB>(P);
         }
-        const float2 dd = dup2(dv[i]), uu = dup2(dv[i] * xv[i]);
-        const bool last = MODE == kLocalBwd && ti + 1 == end && a.dS;
-        float2 acc = dup2(0.f), acc1 = dup2(0.f);
-#pragma unroll
-        for (int p = 0; p < NP; p += 2) {
-          const float4 b4 = *reinterpret_cast<const float4*>(&sB[buf][i][sl * SPT + 2 * p]);
-          const float2 w0 = decay2(dd, A2[p]), w1 = decay2(dd, A2[p + 1]);
-          h[p] = fma2(w0, h[p], mul2(uu, make_float2(b4.x, b4.y)));
-          h[p + 1] = fma2(w1, h[p + 1], mul2(uu, make_float2(b4.z, b4.w)));
-          if (kC) {
-            const float4 c4 = *reinterpret_cast<const float4*>(&sC[kC ? buf : 0][kC ? i : 0][kC ? sl * SPT + 2 * p : 0]);
-            if (MODE == kForward) {
-              acc = fma2(h[p], make_float2(c4.x, c4.y), acc);
-              acc1 = fma2(h[p + 1], make_float2(c4.z, c4.w), acc1);
-            } else {
-              P[p] = mul2(P[p], w0);
-              P[p + 1] = mul2(P[p + 1], w1);
-              float2 g0 = mul2(dup2(gv[i]), make_float2(c4.x, c4.y)), g1 = mul2(dup2(gv[i]), make_float2(c4.z, c4.w));
-              if (last) {
-                const float4 s4 = *reinterpret_cast<const float4*>(a.dS + (long long)n * a.d * S + crow + 2 * p);
-                g0 = add2(g0, make_float2(s4.x, s4.y));
-                g1 = add2(g1, make_float2(s4.z, s4.w));
-              }
-              R[p] = fma2(P[p], g0, R[p]);
-              R[p + 1] = fma2(P[p + 1], g1, R[p + 1]);
-            }
-          }
+        const float xv = to_f32<T>(xp[i * a.xs]);
+        const float delta = softplus_f(to_f32<T>(dtp[i * a.dts]) + bias);
+        float gv = 1.f;
+        if (gated) {
+          const float zz = to_f32<T>(zp[i * a.zs]);
+          gv = zz * fast_sigmoid(zz);
         }
-        part += dv[i];
-        if (MODE == kForward) {
-          acc = add2(acc, acc1);
-          float yy = acc.x + acc.y;
-#pragma unroll
-          for (int o = LPC / 2; o > 0; o >>= 1) yy += __shfl_xor_sync(0xffffffffu, yy, o);
-          yv[i] = fmaf(Dc, xv[i], yy) * gv[i];
-        }
+        if (MODE == kLocalBwd) gv *= to_f32<T>(dyp[(long long)i * a.d]);
+        const float y = token(delta, xv, gv, sB[buf][i], kC ? sC[kC ? buf : 0][kC ? i : 0] : nullptr,
+                              MODE == kLocalBwd && a.dS && t + i + 1 == end);
+        part += delta;
+        if (MODE == kForward && active && sl == 0) yp[(long long)i * a.d] = from_f32<T>(y);
       }
+      if (t + 2 * kTile <= t1)
+        fetch(xp + kTile * a.xs, dtp + kTile * a.dts, gated ? zp + kTile * a.zs : nullptr,
+              MODE == kLocalBwd ? dyp + (long long)kTile * a.d : nullptr);
     }
     sumd += part;
-    if (MODE == kForward && active && sl == 0) {
-      T* yp = static_cast<T*>(a.y) + c;
-#pragma unroll
-      for (int i = 0; i < kTile; ++i)
-        if (t + i < t1) yp[(t + i) * a.d] = from_f32<T>(yv[i]);
-    }
+    xp += kTile * a.xs;
+    dtp += kTile * a.dts;
+    if (gated) zp += kTile * a.zs;
+    if (MODE == kLocalBwd) dyp += (long long)kTile * a.d;
+    if (MODE == kForward) yp += (long long)kTile * a.d;
   }
-  if (MODE == kForward) {
+  if constexpr (MODE == kForward) {
     if (t1 == end && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
   } else if (active) {
     store_state<NP>(a.entry + chunk * a.d * S + crow, h);
-    if (MODE == kLocalBwd) store_state<NP>(a.exitg + chunk * a.d * S + crow, R);
+    if constexpr (MODE == kLocalBwd) store_state<NP>(a.exitg + chunk * a.d * S + crow, R);
     if (sl == 0) a.sumd[chunk * a.d + c] = cut ? -1.f : sumd;
   }
 }
@@ -403,7 +467,7 @@ inline int channel_blocks(int d, int groups, int S) {
 // Chunks of the forward.  A batch whose channels give every SM sub-partition a
 // warp or more runs unsplit (a split costs the exponentials a second time);
 // otherwise, and for packed sequences, the token axis is cut so that about
-// 16 warps an SM run, into chunks of 64 tokens at least.
+// 12 warps an SM run, into chunks of 64 tokens at least.
 struct FwdPlan {
   bool split;
   long long L, chunks;
@@ -414,7 +478,7 @@ inline FwdPlan fwd_plan(long long B, long long T, int num_seqs, int d, int group
   const bool packed = num_seqs > 1;
   if (!packed && (B * warps >= 148 * 4 || T < 128)) return {false, T > 0 ? T : 1, B};
   if (tokens < 128) return {false, tokens > 0 ? tokens : 1, 1};
-  long long chunks = (148 * 16 + warps - 1) / warps;
+  long long chunks = (148 * 12 + warps - 1) / warps;
   long long L = (tokens + chunks - 1) / chunks;
   L = L < 64 ? 64 : (L + kTile - 1) / kTile * kTile;
   chunks = (tokens + L - 1) / L;
