@@ -122,20 +122,20 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
-// One element kept in a 32-bit register as it was loaded (two 16-bit values
-// packed into one register would have to arrive before the packing, which ends
-// the overlap of a load issued ahead).
-template <typename T>
-__device__ __forceinline__ uint32_t load_raw(const T* p);
-template <>
-__device__ __forceinline__ uint32_t load_raw<float>(const float* p) { return __float_as_uint(*p); }
-template <>
-__device__ __forceinline__ uint32_t load_raw<__nv_bfloat16>(const __nv_bfloat16* p) {
-  return *reinterpret_cast<const unsigned short*>(p);
+// Asynchronous copies to shared memory of BYTES (4, 8 or 16, both sides that
+// aligned), the last of them only `bytes` long (the rest is zeroed).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes = BYTES) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(bytes) : "memory");
 }
-template <typename T>
-__device__ __forceinline__ float raw_to_f32(uint32_t r) {
-  return sizeof(T) == 2 ? __uint_as_float(r << 16) : __uint_as_float(r);
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 // Two fp32 lanes in one instruction.

@@ -4,11 +4,13 @@
 //   delta_t = softplus(dt_t + dt_bias);  h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t
 //   y_t = (C_t . h_t + D x_t) silu(z_t)
 //
-// Forward: a thread owns one channel and SPT of its S states (S <= 16: all of
-// them) and walks the tokens with the state in registers; B and C of kTile
-// tokens sit in shared memory in fp32, shared by the channels of the CTA; the
-// tile after is loaded meanwhile.  One exponential per (token, channel, state)
-// bounds it (16 a clock and SM), not HBM: 8 bytes per token and channel.
+// Forward: a lane owns SPT states of one channel (S / SPT lanes a channel) and
+// walks the tokens with them in registers; B and C of kTile tokens sit in shared
+// memory in fp32, shared by the channels of the CTA.  What a (token, channel)
+// needs once (time step, gate, skip, output) is done by one of the channel's
+// lanes, each for its share of kStep tokens.  One exponential per (token,
+// channel, state) bounds it (16 a clock and SM), not HBM: 8 bytes per token and
+// channel.
 //
 // When a batch has too few channels to fill the card, or sequences are packed
 // (their lengths are on the device only), the token axis is cut into chunks
@@ -18,13 +20,17 @@
 // chunk from its entry state.  A chunk in which a sequence starts passes
 // nothing on from before it.
 #pragma once
+#include <initializer_list>
+
 #include "kda_layer_common.cuh"
 
 namespace kda {
 namespace scan {
 
 constexpr int kThreads = 128;
-constexpr int kTile = 8;  // tokens staged at a time
+constexpr int kTile = 16;   // tokens staged at a time
+constexpr int kStep = 8;    // tokens unrolled together
+constexpr int kStages = 3;  // tiles of inputs in shared memory: one in use, two on their way
 
 struct Args {
   const void *x, *dt, *z, *B, *C;
@@ -43,14 +49,43 @@ struct Args {
   const void* dy;    // [tokens, d]
   const float* dS;   // [N, d, S] or nullptr
   float* exitg;      // [chunks, d, S]: as entry, for the gradient that comes from the right
+  bool wide;         // the inputs can be copied 16 bytes at a time
 };
 
 template <int S>
 struct Shape {
-  static constexpr int SPT = S < 16 ? S : 16;   // states a thread
+  static constexpr int SPT = 8;                 // states a lane
   static constexpr int LPC = S / SPT;           // lanes a channel
   static constexpr int CH = kThreads / LPC;     // channels a CTA
+  static constexpr int OWN = kStep / LPC;       // tokens of a step a lane prepares and finishes
 };
+
+// Sum over the NL lanes whose numbers differ in the bits STRIDE, 2 STRIDE, ..
+// of NV values each.  The lane keeps max(1, NV / NL) of the sums in
+// v[0 .. ); *index counts the first one.
+template <int NV, int NL, int STRIDE>
+__device__ __forceinline__ void reduce_scatter(float (&v)[NV], int lane, int* index) {
+  int at = 0;
+  int have = NV;
+#pragma unroll
+  for (int o = NL / 2; o > 0; o >>= 1) {
+    const bool up = (lane & (o * STRIDE)) != 0;
+    if (have > 1) {
+      have >>= 1;
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i)
+        if (i < have) {
+          const float send = up ? v[i] : v[i + have];
+          const float keep = up ? v[i + have] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o * STRIDE);
+        }
+      at += up ? have : 0;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * STRIDE);
+    }
+  }
+  *index = at;
+}
 
 // log(1 + e^v) of two values, to fp32 accuracy also where it is small:
 // max(v, 0) + log1p(e), e = e^-|v| in (0, 1], with log1p(e) / e by its minimax
@@ -108,6 +143,44 @@ __device__ __forceinline__ void zero_state(float2 (&h)[N]) {
 
 enum Mode : int { kForward = 0, kLocal = 1, kLocalBwd = 2 };
 
+// The CTA's inputs of one tile, as they are in memory; B, C in fp32; what the
+// lanes of a channel share.
+template <typename T, int S, int MODE>
+struct alignas(16) TileSmem {
+  static constexpr int CH = Shape<S>::CH;
+  static constexpr int NIN = MODE == 0 ? 3 : MODE == 1 ? 2 : 4;  // x, dt (, z (, dy))
+  T in[kStages][NIN][kTile][CH];
+  T raw[kStages][MODE == 1 ? 1 : 2][kTile][S];  // B, C as they are in memory
+  float B[2][kTile][S];
+  float C[MODE == 1 ? 1 : 2][MODE == 1 ? 1 : kTile][MODE == 1 ? 4 : S];
+  float2 du[kStep][CH];                         // delta, delta x
+  float gv[MODE == 2 ? kStep : 1][CH];          // dy silu(z)
+};
+
+// `rows` rows of `len` elements (len <= WIDTH), `stride` apart, to dst[.][WIDTH]:
+// 16 bytes a copy, or one element each (32-bit ones asynchronously too).
+template <typename T, int WIDTH>
+__device__ __forceinline__ void stage_rows(T (*dst)[WIDTH], const T* src, long long stride, int rows, int len,
+                                           bool wide) {
+  if (wide) {
+    constexpr int PER = 16 / sizeof(T), N = WIDTH / PER;  // copies a row
+#pragma unroll
+    for (int i = 0; i < (kTile * N + kThreads - 1) / kThreads; ++i) {
+      const int e = i * kThreads + (int)threadIdx.x, r = e / N, k = (e % N) * PER;
+      if (r < rows && k < len) copy_async<16>(&dst[r][k], src + r * stride + k, min(16, (len - k) * (int)sizeof(T)));
+    }
+  } else {
+#pragma unroll 1
+    for (int e = threadIdx.x; e < rows * WIDTH; e += kThreads) {
+      const int r = e / WIDTH, k = e % WIDTH;
+      if (k < len) {
+        if constexpr (sizeof(T) == 4) copy_async<4>(&dst[r][k], src + r * stride + k);
+        else dst[r][k] = src[r * stride + k];
+      }
+    }
+  }
+}
+
 // MODE kForward: the scan of each chunk from its entry state (S0 where a
 //   sequence starts).  kLocal: the end state of each chunk from zero and the sum
 //   of its deltas.  kLocalBwd: also the gradient that a chunk sends to the state
@@ -115,28 +188,29 @@ enum Mode : int { kForward = 0, kLocal = 1, kLocalBwd = 2 };
 //     sum_t (prod_{s <= t} a_s) C_t dyy_t,  dyy = dy silu(z), up to the first
 //   sequence start in the chunk.
 //
-// A tile of kTile tokens inside one sequence runs without a branch, so that the
-// exponentials of later tokens cover the chains of earlier ones, on inputs
-// loaded a tile ahead; a tile in which a sequence ends, or a last one that is
-// not full, goes token by token.
+// Inputs arrive by asynchronous copies, two tiles ahead.  kStep tokens inside
+// one sequence run without a branch, so that the exponentials of later tokens
+// cover the chains of earlier ones; a step in which a sequence ends, or a last
+// one that is not full, goes token by token.
 template <typename T, int S, int MODE>
-__global__ void __launch_bounds__(kThreads, MODE == kLocal ? 4 : MODE == kForward ? 3 : 2)
-    kda_selective_scan_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selective_scan_kernel(const Args a) {
   using Sh = Shape<S>;
-  constexpr int SPT = Sh::SPT, LPC = Sh::LPC, NP = SPT / 2;
+  constexpr int SPT = Sh::SPT, LPC = Sh::LPC, NP = SPT / 2, CH = Sh::CH, OWN = Sh::OWN;
   constexpr bool kC = MODE != kLocal, kZ = MODE != kLocal;
-  constexpr int NBC = kTile * S / kThreads > 0 ? kTile * S / kThreads : 1;  // staged B (or C) elements a thread
-  __shared__ __align__(16) float sB[2][kTile][S];
-  __shared__ __align__(16) float sC[kC ? 2 : 1][kC ? kTile : 1][kC ? S : 4];
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  TileSmem<T, S, MODE>& sm = *reinterpret_cast<TileSmem<T, S, MODE>*>(smem_raw);
 
   const int cb = (int)(blockIdx.x % a.ncb);
   const long long chunk = blockIdx.x / a.ncb;
   const int grp = cb / a.blocks_per_group;
-  const int cl = (cb % a.blocks_per_group) * Sh::CH + (int)threadIdx.x / LPC;
+  const int cl0 = (cb % a.blocks_per_group) * CH;
+  const int lane = threadIdx.x & 31;
+  const int ch = (int)threadIdx.x / LPC;
   const int sl = (int)threadIdx.x % LPC;
-  const bool active = cl < a.cpg;
-  const int c = grp * a.cpg + (active ? cl : a.cpg - 1);
-  const long long crow = (long long)c * S + sl * SPT;
+  const int width = a.cpg - cl0 < CH ? a.cpg - cl0 : CH;  // channels of the CTA
+  const bool active = ch < width;  // the others compute on whatever shared memory holds and write nothing
+  const long long c0 = (long long)grp * a.cpg + cl0, c = c0 + (active ? ch : width - 1);
+  const long long crow = c * S + sl * SPT;
 
   if (blockIdx.x == 0) check_seq_table(a.q);
   if (MODE == kForward && chunk == 0 && a.S_out) {  // sequences without tokens keep their state
@@ -151,6 +225,41 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocal ? 4 : MODE == kForwar
   const long long t0 = chunk * a.L;
   const long long t1 = t0 + a.L < a.q.total ? t0 + a.L : a.q.total;
   if (t0 >= t1) return;
+  const bool gated = kZ && a.z;
+
+  auto stage = [&](long long t, int st) {
+    if (t < t1) {
+      const int rows = t1 - t < kTile ? (int)(t1 - t) : kTile;
+      stage_rows<T, CH>(sm.in[st][0], static_cast<const T*>(a.x) + t * a.xs + c0, a.xs, rows, width, a.wide);
+      stage_rows<T, CH>(sm.in[st][1], static_cast<const T*>(a.dt) + t * a.dts + c0, a.dts, rows, width, a.wide);
+      if constexpr (kZ)
+        if (gated)
+          stage_rows<T, CH>(sm.in[st][kZ ? 2 : 0], static_cast<const T*>(a.z) + t * a.zs + c0, a.zs, rows, width,
+                            a.wide);
+      if constexpr (MODE == kLocalBwd)
+        stage_rows<T, CH>(sm.in[st][MODE == kLocalBwd ? 3 : 0], static_cast<const T*>(a.dy) + t * a.d + c0, a.d, rows,
+                          width, a.wide);
+      stage_rows<T, S>(sm.raw[st][0], static_cast<const T*>(a.B) + t * a.bs + (long long)grp * S, a.bs, rows, S,
+                       a.wide);
+      if constexpr (kC)
+        stage_rows<T, S>(sm.raw[st][kC ? 1 : 0], static_cast<const T*>(a.C) + t * a.cs + (long long)grp * S, a.cs, rows,
+                         S, a.wide);
+    }
+    copy_async_commit();
+  };
+  // B, C of a tile in fp32 (a barrier before and after); rows past the chunk are not used
+  auto convert = [&](int st, int buf) {
+#pragma unroll
+    for (int i = 0; i < (kTile * S + kThreads - 1) / kThreads; ++i) {
+      const int e = i * kThreads + (int)threadIdx.x;
+      if (e < kTile * S) {
+        (&sm.B[buf][0][0])[e] = to_f32<T>((&sm.raw[st][0][0][0])[e]);
+        if constexpr (kC) (&sm.C[kC ? buf : 0][0][0])[e] = to_f32<T>((&sm.raw[st][kC ? 1 : 0][0][0])[e]);
+      }
+    }
+  };
+  stage(t0, 0);
+  stage(t0 + kTile, 1);
 
   float2 A2[NP], h[NP];
   load_state<NP>(a.A + crow, A2);
@@ -158,7 +267,6 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocal ? 4 : MODE == kForwar
   for (int i = 0; i < NP; ++i) A2[i] = mul2(A2[i], dup2(kLog2eF));
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
   const float Dc = kC && a.Dv ? a.Dv[c] : 0.f;
-  const bool gated = kZ && a.z;
 
   int n = seq_of_token(a.q, t0);
   long long end = seq_end(a.q, n);
@@ -170,39 +278,32 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocal ? 4 : MODE == kForwar
   float2 P[NPB], R[NPB];  // kLocalBwd: product of the decays so far, gradient sent to the left
 #pragma unroll
   for (int i = 0; i < NPB; ++i) P[i] = dup2(cut ? 0.f : 1.f), R[i] = dup2(0.f);
-  float sumd = 0.f;
+  float sumd = 0.f;  // of the tokens that this lane prepares
 
-  const T* xp = static_cast<const T*>(a.x) + t0 * a.xs + c;
-  const T* dtp = static_cast<const T*>(a.dt) + t0 * a.dts + c;
-  const T* zp = gated ? static_cast<const T*>(a.z) + t0 * a.zs + c : nullptr;
-  const T* dyp = MODE == kLocalBwd ? static_cast<const T*>(a.dy) + t0 * a.d + c : nullptr;
-  T* yp = MODE == kForward ? static_cast<T*>(a.y) + t0 * a.d + c : nullptr;
+  // the first of the lane's own tokens of a step, as reduce_scatter deals them
+  int own0 = 0;
+  {
+    int have = kStep;
+#pragma unroll
+    for (int o = LPC / 2; o > 0; o >>= 1) {
+      have >>= 1;
+      own0 += (sl & o) ? have : 0;
+    }
+  }
 
-  uint32_t rx[kTile], rdt[kTile], rz[kTile], rdy[MODE == kLocalBwd ? kTile : 1], rB[NBC], rC[NBC];
-  auto fetch_bc = [&](long long t) {  // tokens past the chunk repeat its last one and are not used
-#pragma unroll
-    for (int i = 0; i < NBC; ++i) {
-      const int e = i * kThreads + (int)threadIdx.x;
-      const long long tt = t + e / S < t1 ? t + e / S : t1 - 1;
-      if (e < kTile * S) {
-        rB[i] = load_raw<T>(static_cast<const T*>(a.B) + tt * a.bs + (long long)grp * S + e % S);
-        if (kC) rC[i] = load_raw<T>(static_cast<const T*>(a.C) + tt * a.cs + (long long)grp * S + e % S);
-      }
-    }
+  auto next_sequence = [&](long long t) {
+    if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
+    n = seq_of_token(a.q, t);
+    end = seq_end(a.q, n);
+    cut = true;
+    if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
+    else zero_state<NP>(h);
+    if (MODE == kLocalBwd) zero_state<NPB>(P);
   };
-  auto fetch = [&](const T* px, const T* pdt, const T* pz, const T* pdy) {
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      rx[i] = load_raw<T>(px + i * a.xs);
-      rdt[i] = load_raw<T>(pdt + i * a.dts);
-      if (gated) rz[i] = load_raw<T>(pz + i * a.zs);
-      if (MODE == kLocalBwd) rdy[i] = load_raw<T>(pdy + (long long)i * a.d);
-    }
-  };
-  // one token: gv is the gate (kForward) or dy times it (kLocalBwd); last: with the final state's gradient
-  auto token = [&](float delta, float xv, float gv, const float* tb, const float* tc, bool last) -> float {
-    const float2 dd = dup2(delta), uu = dup2(delta * xv);
-    float2 acc = dup2(0.f), acc1 = dup2(0.f);
+  // one token of the lane's states -> its part of C . h.  gv: dy silu(z) (kLocalBwd); last: with dS
+  auto token = [&](float delta, float u, float gv, const float* tb, const float* tc, bool last) -> float {
+    const float2 dd = dup2(delta), uu = dup2(u);
+    float2 acc = dup2(0.f);
 #pragma unroll
     for (int p = 0; p < NP; p += 2) {
       const float4 b4 = *reinterpret_cast<const float4*>(tb + sl * SPT + 2 * p);
@@ -213,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocal ? 4 : MODE == kForwar
         const float4 c4 = *reinterpret_cast<const float4*>(tc + sl * SPT + 2 * p);
         if constexpr (MODE == kForward) {
           acc = fma2(h[p], make_float2(c4.x, c4.y), acc);
-          acc1 = fma2(h[p + 1], make_float2(c4.z, c4.w), acc1);
+          acc = fma2(h[p + 1], make_float2(c4.z, c4.w), acc);
         } else {
           P[p] = mul2(P[p], w0);
           P[p + 1] = mul2(P[p + 1], w1);
@@ -228,109 +329,105 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocal ? 4 : MODE == kForwar
         }
       }
     }
-    if (MODE != kForward) return 0.f;
-    acc = add2(acc, acc1);
-    float yy = acc.x + acc.y;
-#pragma unroll
-    for (int o = LPC / 2; o > 0; o >>= 1) yy += __shfl_xor_sync(0xffffffffu, yy, o);
-    return fmaf(Dc, xv, yy) * gv;
+    return acc.x + acc.y;
   };
 
-  fetch_bc(t0);
-  if (t0 + kTile <= t1) fetch(xp, dtp, zp, dyp);
-  int buf = 0;
-  for (long long t = t0; t < t1; t += kTile, buf ^= 1) {
-#pragma unroll
-    for (int i = 0; i < NBC; ++i) {
-      const int e = i * kThreads + (int)threadIdx.x;
-      if (e < kTile * S) {
-        (&sB[buf][0][0])[e] = raw_to_f32<T>(rB[i]);
-        if (kC) (&sC[kC ? buf : 0][0][0])[e] = raw_to_f32<T>(rC[i]);
-      }
-    }
-    __syncthreads();  // the other buffer is free: its readers passed this point a tile ago
-    if (t + kTile < t1) fetch_bc(t + kTile);
-    if (t == end) {  // the first token of another sequence
-      if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
-      n = seq_of_token(a.q, t);
-      end = seq_end(a.q, n);
-      cut = true;
-      if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
-      else zero_state<NP>(h);
-      if (MODE == kLocalBwd) zero_state<NPB>(P);
-    }
-    float part = 0.f;
-    // a final state's gradient is added at its sequence's last token, so that tile goes token by token too
-    if (t + kTile <= t1 && (t >= end || t + kTile + (MODE == kLocalBwd) <= end)) {
-      float xv[kTile], dv[kTile], gv[kTile];
-#pragma unroll
-      for (int i = 0; i < kTile; i += 2) {
-        const float2 d2 = softplus2(add2(make_float2(raw_to_f32<T>(rdt[i]), raw_to_f32<T>(rdt[i + 1])), dup2(bias)));
-        dv[i] = d2.x;
-        dv[i + 1] = d2.y;
-      }
-#pragma unroll
-      for (int i = 0; i < kTile; ++i) {
-        xv[i] = raw_to_f32<T>(rx[i]);
-        gv[i] = 1.f;
-        if (gated) {
-          const float zz = raw_to_f32<T>(rz[i]);
-          gv[i] = zz * fast_sigmoid(zz);
-        }
-        if (MODE == kLocalBwd) gv[i] *= raw_to_f32<T>(rdy[i]);
-      }
-      if (t + 2 * kTile <= t1)
-        fetch(xp + kTile * a.xs, dtp + kTile * a.dts, gated ? zp + kTile * a.zs : nullptr,
-              MODE == kLocalBwd ? dyp + (long long)kTile * a.d : nullptr);
-#pragma unroll
-      for (int i = 0; i < kTile; ++i) {
-        const float y = token(dv[i], xv[i], gv[i], sB[buf][i], kC ? sC[kC ? buf : 0][kC ? i : 0] : nullptr, false);
-        part += dv[i];
-        if (MODE == kForward && active && sl == 0) yp[(long long)i * a.d] = from_f32<T>(y);
-      }
-    } else {
-      const int m = t1 - t < kTile ? (int)(t1 - t) : kTile;
+  copy_async_wait<1>();
+  __syncthreads();
+  convert(0, 0);
+  int buf = 0, st = 0;
+  for (long long t = t0; t < t1; t += kTile) {
+    copy_async_wait<0>();  // the next tile's copies of this thread
+    __syncthreads();       // ... of all threads; this tile's B, C; and the stage after next is free
+    const int st1 = st + 1 < kStages ? st + 1 : 0, st2 = st1 + 1 < kStages ? st1 + 1 : 0;
+    stage(t + 2 * kTile, st2);
+    if (t + kTile < t1) convert(st1, buf ^ 1);
+    const T(*in)[kTile][CH] = sm.in[st];
 #pragma unroll 1
-      for (int i = 0; i < m; ++i) {
-        if (i > 0 && t + i == end) {
-          if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
-          n = seq_of_token(a.q, t + i);
-          end = seq_end(a.q, n);
-          cut = true;
-          if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
-          else zero_state<NP>(h);
-          if (MODE == kLocalBwd) zero_state<NPB>(P);
+    for (int s0 = 0; s0 < kTile && t + s0 < t1; s0 += kStep) {
+      const long long ts = t + s0;
+      if (ts == end) next_sequence(ts);  // the first token of another sequence
+      T* yp = MODE == kForward ? static_cast<T*>(a.y) + ts * a.d + c : nullptr;
+      // a final state's gradient is added at its sequence's last token, so that step goes token by token too
+      if (ts + kStep <= t1 && (ts >= end || ts + kStep + (MODE == kLocalBwd) <= end)) {
+        float xv[OWN], gv[OWN], dv[OWN];
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) dv[j] = to_f32<T>(in[1][s0 + own0 + j][ch]) + bias;
+#pragma unroll
+        for (int j = 0; j < OWN; j += 2) {
+          const float2 d2 = softplus2(make_float2(dv[j], dv[OWN > 1 ? j + 1 : j]));
+          dv[j] = d2.x;
+          if (OWN > 1) dv[OWN > 1 ? j + 1 : j] = d2.y;
         }
-        const float xv = to_f32<T>(xp[i * a.xs]);
-        const float delta = softplus_f(to_f32<T>(dtp[i * a.dts]) + bias);
-        float gv = 1.f;
-        if (gated) {
-          const float zz = to_f32<T>(zp[i * a.zs]);
-          gv = zz * fast_sigmoid(zz);
+        __syncwarp();  // the step before has been read
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+          const int i = own0 + j;
+          xv[j] = to_f32<T>(in[0][s0 + i][ch]);
+          gv[j] = 1.f;
+          if (gated) {
+            const float zz = to_f32<T>(in[kZ ? 2 : 0][s0 + i][ch]);
+            gv[j] = zz * fast_sigmoid(zz);
+          }
+          if constexpr (MODE == kLocalBwd)
+            sm.gv[MODE == kLocalBwd ? i : 0][ch] = gv[j] * to_f32<T>(in[MODE == kLocalBwd ? 3 : 0][s0 + i][ch]);
+          sm.du[i][ch] = make_float2(dv[j], dv[j] * xv[j]);
+          sumd += dv[j];
         }
-        if (MODE == kLocalBwd) gv *= to_f32<T>(dyp[(long long)i * a.d]);
-        const float y = token(delta, xv, gv, sB[buf][i], kC ? sC[kC ? buf : 0][kC ? i : 0] : nullptr,
-                              MODE == kLocalBwd && a.dS && t + i + 1 == end);
-        part += delta;
-        if (MODE == kForward && active && sl == 0) yp[(long long)i * a.d] = from_f32<T>(y);
+        __syncwarp();
+        float yv[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+          const float2 du = sm.du[i][ch];
+          yv[i] = token(du.x, du.y, MODE == kLocalBwd ? sm.gv[MODE == kLocalBwd ? i : 0][ch] : 0.f, sm.B[buf][s0 + i],
+                        kC ? sm.C[kC ? buf : 0][kC ? s0 + i : 0] : nullptr, false);
+        }
+        if constexpr (MODE == kForward) {
+          int at;
+          reduce_scatter<kStep, LPC, 1>(yv, lane, &at);
+          if (active) {
+#pragma unroll
+            for (int j = 0; j < OWN; ++j)
+              yp[(long long)(own0 + j) * a.d] = from_f32<T>(fmaf(Dc, xv[j], yv[j]) * gv[j]);
+          }
+        }
+      } else {
+        const int m = t1 - ts < kStep ? (int)(t1 - ts) : kStep;
+#pragma unroll 1
+        for (int i = 0; i < m; ++i) {
+          if (i > 0 && ts + i == end) next_sequence(ts + i);
+          const float xv = to_f32<T>(in[0][s0 + i][ch]);
+          const float delta = softplus_f(to_f32<T>(in[1][s0 + i][ch]) + bias);
+          float gv = 1.f;
+          if (gated) {
+            const float zz = to_f32<T>(in[kZ ? 2 : 0][s0 + i][ch]);
+            gv = zz * fast_sigmoid(zz);
+          }
+          if (MODE == kLocalBwd) gv *= to_f32<T>(in[MODE == kLocalBwd ? 3 : 0][s0 + i][ch]);
+          float y = token(delta, delta * xv, gv, sm.B[buf][s0 + i], kC ? sm.C[kC ? buf : 0][kC ? s0 + i : 0] : nullptr,
+                          MODE == kLocalBwd && a.dS && ts + i + 1 == end);
+          if (sl == 0) sumd += delta;
+          if (MODE == kForward) {
+#pragma unroll
+            for (int o = LPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            if (active && sl == 0) yp[(long long)i * a.d] = from_f32<T>(fmaf(Dc, xv, y) * gv);
+          }
+        }
       }
-      if (t + 2 * kTile <= t1)
-        fetch(xp + kTile * a.xs, dtp + kTile * a.dts, gated ? zp + kTile * a.zs : nullptr,
-              MODE == kLocalBwd ? dyp + (long long)kTile * a.d : nullptr);
     }
-    sumd += part;
-    xp += kTile * a.xs;
-    dtp += kTile * a.dts;
-    if (gated) zp += kTile * a.zs;
-    if (MODE == kLocalBwd) dyp += (long long)kTile * a.d;
-    if (MODE == kForward) yp += (long long)kTile * a.d;
+    buf ^= 1;
+    st = st1;
   }
   if constexpr (MODE == kForward) {
     if (t1 == end && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
-  } else if (active) {
-    store_state<NP>(a.entry + chunk * a.d * S + crow, h);
-    if constexpr (MODE == kLocalBwd) store_state<NP>(a.exitg + chunk * a.d * S + crow, R);
-    if (sl == 0) a.sumd[chunk * a.d + c] = cut ? -1.f : sumd;
+  } else {
+#pragma unroll
+    for (int o = LPC / 2; o > 0; o >>= 1) sumd += __shfl_xor_sync(0xffffffffu, sumd, o);
+    if (active) {
+      store_state<NP>(a.entry + chunk * a.d * S + crow, h);
+      if constexpr (MODE == kLocalBwd) store_state<NP>(a.exitg + chunk * a.d * S + crow, R);
+      if (sl == 0) a.sumd[chunk * a.d + c] = cut ? -1.f : sumd;
+    }
   }
 }
 
@@ -458,7 +555,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) kda_selective_scan_step_kerne
 // Host
 // ---------------------------------------------------------------------------
 inline bool supported_state(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }
-inline int lanes_per_channel(int S) { return S <= 16 ? 1 : S / 16; }
+inline int lanes_per_channel(int S) { return S / 8; }
 inline int channel_blocks(int d, int groups, int S) {
   const int ch = kThreads / lanes_per_channel(S);
   return groups * ((d / groups + ch - 1) / ch);
@@ -467,18 +564,29 @@ inline int channel_blocks(int d, int groups, int S) {
 // Chunks of the forward.  A batch whose channels give every SM sub-partition a
 // warp or more runs unsplit (a split costs the exponentials a second time);
 // otherwise, and for packed sequences, the token axis is cut so that about
-// 12 warps an SM run, into chunks of 64 tokens at least.
+// 16 warps an SM run at once, into chunks of 64 tokens at least.
 struct FwdPlan {
   bool split;
   long long L, chunks;
 };
+// Whether the inputs' addresses and strides allow copies of 16 bytes.  A CTA's
+// channels start at a multiple of 16 of their group.
+inline bool wide_copies(const Args& a, int esize) {
+  const long long per = 16 / esize;
+  uintptr_t low = 0;
+  for (const void* p : {a.x, a.dt, a.z, a.B, a.C, a.dy}) low |= reinterpret_cast<uintptr_t>(p);
+  bool ok = low % 16 == 0 && (a.cpg == a.d || a.cpg % per == 0) && (!a.dy || a.d % per == 0);
+  for (const long long s : {a.xs, a.dts, a.z ? a.zs : 0LL, a.bs, a.cs}) ok = ok && s % per == 0;
+  return ok;
+}
 inline FwdPlan fwd_plan(long long B, long long T, int num_seqs, int d, int groups, int S) {
   const long long tokens = B * T;
   const long long warps = (long long)channel_blocks(d, groups, S) * (kThreads / 32);
   const bool packed = num_seqs > 1;
-  if (!packed && (B * warps >= 148 * 4 || T < 128)) return {false, T > 0 ? T : 1, B};
+  if (!packed && (B * warps >= 148 * 8 || T < 128)) return {false, T > 0 ? T : 1, B};
   if (tokens < 128) return {false, tokens > 0 ? tokens : 1, 1};
-  long long chunks = (148 * 12 + warps - 1) / warps;
+  long long chunks = 148 * 16 / warps;
+  if (chunks < 1) chunks = 1;
   long long L = (tokens + chunks - 1) / chunks;
   L = L < 64 ? 64 : (L + kTile - 1) / kTile * kTile;
   chunks = (tokens + L - 1) / L;
@@ -490,7 +598,17 @@ template <typename T, int S, int MODE>
 cudaError_t launch_scan(Args a, cudaStream_t st) {
   const long long grid = a.chunks * a.ncb;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kda_selective_scan_kernel<T, S, MODE><<<(unsigned)grid, kThreads, 0, st>>>(a);
+  a.wide = wide_copies(a, (int)sizeof(T));
+  constexpr size_t bytes = sizeof(TileSmem<T, S, MODE>);
+  if (bytes > 48 * 1024) {
+    static PerDeviceOnce once;
+    const cudaError_t e = run_once_per_device(once, [] {
+      return cudaFuncSetAttribute(kda_selective_scan_kernel<T, S, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)bytes);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  kda_selective_scan_kernel<T, S, MODE><<<(unsigned)grid, kThreads, bytes, st>>>(a);
   return cudaGetLastError();
 }
 inline cudaError_t launch_carry(const Args& a, int S, bool both, cudaStream_t st) {

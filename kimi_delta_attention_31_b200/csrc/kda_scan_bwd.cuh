@@ -41,33 +41,6 @@ struct BwdOut {
   int groups;
 };
 
-// Sum over the NL lanes whose numbers differ in the bits STRIDE, 2 STRIDE, ..
-// of NV values each.  The lane keeps max(1, NV / NL) of the sums in
-// v[0 .. ); *index counts the first one.
-template <int NV, int NL, int STRIDE>
-__device__ __forceinline__ void reduce_scatter(float (&v)[NV], int lane, int* index) {
-  int at = 0;
-  int have = NV;
-#pragma unroll
-  for (int o = NL / 2; o > 0; o >>= 1) {
-    const bool up = (lane & (o * STRIDE)) != 0;
-    if (have > 1) {
-      have >>= 1;
-#pragma unroll
-      for (int i = 0; i < NV / 2; ++i)
-        if (i < have) {
-          const float send = up ? v[i] : v[i + have];
-          const float keep = up ? v[i + have] : v[i];
-          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o * STRIDE);
-        }
-      at += up ? have : 0;
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * STRIDE);
-    }
-  }
-  *index = at;
-}
-
 template <int S>
 struct BwdShape {
   static constexpr int LPC = S / 4;        // lanes a channel
