@@ -153,7 +153,7 @@ struct alignas(16) TileSmem {
   T raw[kStages][MODE == 1 ? 1 : 2][kTile][S];  // B, C as they are in memory
   float B[2][kTile][S];
   float C[MODE == 1 ? 1 : 2][MODE == 1 ? 1 : kTile][MODE == 1 ? 4 : S];
-  float2 du[kStep][CH];                         // delta, delta x
+  float4 du[kStep][CH];                         // delta twice, delta x twice
   float gv[MODE == 2 ? kStep : 1][CH];          // dy silu(z)
 };
 
@@ -193,7 +193,7 @@ __device__ __forceinline__ void stage_rows(T (*dst)[WIDTH], const T* src, long l
 // cover the chains of earlier ones; a step in which a sequence ends, or a last
 // one that is not full, goes token by token.
 template <typename T, int S, int MODE>
-__global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selective_scan_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const Args a) {
   using Sh = Shape<S>;
   constexpr int SPT = Sh::SPT, LPC = Sh::LPC, NP = SPT / 2, CH = Sh::CH, OWN = Sh::OWN;
   constexpr bool kC = MODE != kLocal, kZ = MODE != kLocal;
@@ -291,6 +291,8 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selec
     }
   }
 
+  T* yp = MODE == kForward ? static_cast<T*>(a.y) + (t0 + own0) * a.d + c : nullptr;
+
   auto next_sequence = [&](long long t) {
     if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
     n = seq_of_token(a.q, t);
@@ -301,8 +303,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selec
     if (MODE == kLocalBwd) zero_state<NPB>(P);
   };
   // one token of the lane's states -> its part of C . h.  gv: dy silu(z) (kLocalBwd); last: with dS
-  auto token = [&](float delta, float u, float gv, const float* tb, const float* tc, bool last) -> float {
-    const float2 dd = dup2(delta), uu = dup2(u);
+  auto token = [&](float2 dd, float2 uu, float gv, const float* tb, const float* tc, bool last) -> float {
     float2 acc = dup2(0.f);
 #pragma unroll
     for (int p = 0; p < NP; p += 2) {
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selec
       if constexpr (kC) {
         const float4 c4 = *reinterpret_cast<const float4*>(tc + sl * SPT + 2 * p);
         if constexpr (MODE == kForward) {
-          acc = fma2(h[p], make_float2(c4.x, c4.y), acc);
+          acc = p == 0 ? mul2(h[p], make_float2(c4.x, c4.y)) : fma2(h[p], make_float2(c4.x, c4.y), acc);
           acc = fma2(h[p + 1], make_float2(c4.z, c4.w), acc);
         } else {
           P[p] = mul2(P[p], w0);
@@ -347,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selec
     for (int s0 = 0; s0 < kTile && t + s0 < t1; s0 += kStep) {
       const long long ts = t + s0;
       if (ts == end) next_sequence(ts);  // the first token of another sequence
-      T* yp = MODE == kForward ? static_cast<T*>(a.y) + ts * a.d + c : nullptr;
       // a final state's gradient is added at its sequence's last token, so that step goes token by token too
       if (ts + kStep <= t1 && (ts >= end || ts + kStep + (MODE == kLocalBwd) <= end)) {
         float xv[OWN], gv[OWN], dv[OWN];
@@ -371,15 +371,15 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selec
           }
           if constexpr (MODE == kLocalBwd)
             sm.gv[MODE == kLocalBwd ? i : 0][ch] = gv[j] * to_f32<T>(in[MODE == kLocalBwd ? 3 : 0][s0 + i][ch]);
-          sm.du[i][ch] = make_float2(dv[j], dv[j] * xv[j]);
+          sm.du[i][ch] = make_float4(dv[j], dv[j], dv[j] * xv[j], dv[j] * xv[j]);
           sumd += dv[j];
         }
         __syncwarp();
         float yv[kStep];
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
-          const float2 du = sm.du[i][ch];
-          yv[i] = token(du.x, du.y, MODE == kLocalBwd ? sm.gv[MODE == kLocalBwd ? i : 0][ch] : 0.f, sm.B[buf][s0 + i],
+          const float4 du = sm.du[i][ch];
+          yv[i] = token(make_float2(du.x, du.y), make_float2(du.z, du.w), MODE == kLocalBwd ? sm.gv[MODE == kLocalBwd ? i : 0][ch] : 0.f, sm.B[buf][s0 + i],
                         kC ? sm.C[kC ? buf : 0][kC ? s0 + i : 0] : nullptr, false);
         }
         if constexpr (MODE == kForward) {
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selec
           if (active) {
 #pragma unroll
             for (int j = 0; j < OWN; ++j)
-              yp[(long long)(own0 + j) * a.d] = from_f32<T>(fmaf(Dc, xv[j], yv[j]) * gv[j]);
+              yp[(long long)j * a.d] = from_f32<T>(fmaf(Dc, xv[j], yv[j]) * gv[j]);
           }
         }
       } else {
@@ -404,16 +404,17 @@ __global__ void __launch_bounds__(kThreads, MODE == kLocalBwd ? 4 : 5) kda_selec
             gv = zz * fast_sigmoid(zz);
           }
           if (MODE == kLocalBwd) gv *= to_f32<T>(in[MODE == kLocalBwd ? 3 : 0][s0 + i][ch]);
-          float y = token(delta, delta * xv, gv, sm.B[buf][s0 + i], kC ? sm.C[kC ? buf : 0][kC ? s0 + i : 0] : nullptr,
+          float y = token(dup2(delta), dup2(delta * xv), gv, sm.B[buf][s0 + i], kC ? sm.C[kC ? buf : 0][kC ? s0 + i : 0] : nullptr,
                           MODE == kLocalBwd && a.dS && ts + i + 1 == end);
           if (sl == 0) sumd += delta;
           if (MODE == kForward) {
 #pragma unroll
             for (int o = LPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if (active && sl == 0) yp[(long long)i * a.d] = from_f32<T>(fmaf(Dc, xv, y) * gv);
+            if (active && sl == 0) yp[(long long)(i - own0) * a.d] = from_f32<T>(fmaf(Dc, xv, y) * gv);
           }
         }
       }
+      if (MODE == kForward) yp += (long long)kStep * a.d;
     }
     buf ^= 1;
     st = st1;
