@@ -54,7 +54,7 @@ struct Args {
 
 template <int S>
 struct Shape {
-  static constexpr int SPT = 8;                 // states a lane
+  static constexpr int SPT = S <= 16 ? 8 : 16;  // states a lane
   static constexpr int LPC = S / SPT;           // lanes a channel
   static constexpr int CH = kThreads / LPC;     // channels a CTA
   static constexpr int OWN = kStep / LPC;       // tokens of a step a lane prepares and finishes
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) kda_selective_scan_step_kerne
 // Host
 // ---------------------------------------------------------------------------
 inline bool supported_state(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }
-inline int lanes_per_channel(int S) { return S / 8; }
+inline int lanes_per_channel(int S) { return S <= 16 ? S / 8 : S / 16; }
 inline int channel_blocks(int d, int groups, int S) {
   const int ch = kThreads / lanes_per_channel(S);
   return groups * ((d / groups + ch - 1) / ch);

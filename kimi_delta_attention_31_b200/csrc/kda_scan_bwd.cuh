@@ -16,11 +16,13 @@
 // the states that enter them stay in registers between the forward and the
 // reverse sweep, so an exponential is taken once; the warps of a CTA are
 // chained through shared memory the way the tiles are.  dB and dC are sums over
-// channels: the lanes of a warp that hold the same state are summed by
-// exchanges that halve the number of values at each step, and the result stays
-// in registers over all the CTA's channels.  Sums over tokens or channel blocks
-// leave as lines that a second kernel adds in order.
+// channels: every lane adds up its own over all the channels that it works on,
+// and the lanes of a warp that hold the same state are summed once at the end
+// (summing them for every token took a quarter of the instructions).  Sums over
+// tokens or channel blocks leave as lines that a second kernel adds in order.
 #pragma once
+#include <type_traits>
+
 #include "kda_scan.cuh"
 
 namespace kda {
@@ -45,25 +47,30 @@ template <int S>
 struct BwdShape {
   static constexpr int LPC = S / 4;        // lanes a channel
   static constexpr int CPW = 32 / LPC;     // channels a warp at a time
-  static constexpr int ACC = 8 / CPW > 0 ? 8 / CPW : 1;  // dB, dC sums a lane keeps of a token
+  static constexpr int ACC = 8 / CPW > 0 ? 8 / CPW : 1;  // dB, dC sums a lane keeps of a token at the end
   static constexpr int BT = LPC < 4 ? LPC : 4;           // tokens whose state sums are exchanged together
 };
 
 template <int S>
 struct alignas(16) BwdSmem {
   float B[kTokens][S], C[kTokens][S];
-  float delta[kTokens][kSlab], u[kTokens][kSlab], dyy[kTokens][kSlab];
+  float4 du[kTokens][kSlab];   // delta twice, delta x twice
+  float2 dyy[kTokens][kSlab];  // twice
   float sA[kTokens][kSlab], gB[kTokens][kSlab], yy[kTokens][kSlab];
-  float P[kWarps][128], H[kWarps][128], R[kWarps][128], dA[kWarps][128];
+  float P[kWarps][128], H[kWarps][128], R[kWarps][128], dA[2][kWarps][128];
   float ch[kWarps][2][kSlab];
   int first[kTokens], last[kTokens];  // the sequence that starts / ends at this token, or -1
-  int cut[kWarps];                    // a sequence starts in the warp's tokens
+  int cut;                            // bit w: a sequence starts in the tokens of warp w
 };
 
+__device__ __forceinline__ float2 lo2(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi2(float4 v) { return make_float2(v.z, v.w); }
+
 template <typename T, int S>
-__global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(const Args a, const BwdOut o) {
+__global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(const Args a, const BwdOut o) {
   using Sh = BwdShape<S>;
   constexpr int LPC = Sh::LPC, CPW = Sh::CPW, ACC = Sh::ACC, BT = Sh::BT;
+  constexpr int kSteps = kSlab / CPW;  // of a slab
   extern __shared__ __align__(16) unsigned char smem_raw[];
   BwdSmem<S>& s = *reinterpret_cast<BwdSmem<S>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -74,7 +81,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
   const long long t0 = tile * kTokens;
   const int live = (int)(a.q.total - t0 < kTokens ? a.q.total - t0 : kTokens);
   const int tw = warp * kRun;  // the warp's first token in the tile
+  const long long gch = (long long)grp * a.cpg;  // the group's first channel
 
+  if (tid == 0) s.cut = 0;
   if (tid < kTokens) {
     int f = -1, l = -1;
     if (tid < live) {
@@ -96,25 +105,39 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
     s.C[t][k] = cc;
   }
   __syncthreads();
-  if (lane == 0) {
-    int any = 0;
+  bool starts = false, edges = false;
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) any |= s.first[tw + k] >= 0;
-    s.cut[warp] = any;
+  for (int k = 0; k < kRun; ++k) {
+    starts |= s.first[tw + k] >= 0;
+    edges |= s.last[tw + k] >= 0;
   }
+  edges |= starts;
+  if (lane == 0 && starts) atomicOr(&s.cut, 1 << warp);  // read after the next barrier
 
-  float acc[kRun][ACC];
+  // dB and dC of the lane's four states, for each of the warp's tokens, over the lane's channels
+  float2 accB[kRun][2], accC[kRun][2];
 #pragma unroll
-  for (int k = 0; k < kRun; ++k)
-#pragma unroll
-    for (int j = 0; j < ACC; ++j) acc[k][j] = 0.f;
+  for (int k = 0; k < kRun; ++k) accB[k][0] = accB[k][1] = accC[k][0] = accC[k][1] = dup2(0.f);
+
+  // first of the four states of this lane in step `step` of the slab at channel slab0 of the group (the last
+  // channel again past the group's end), and of the element that this thread chains
+  auto lane_row = [&](int slab0, int step) {
+    const int cin = slab0 + step * CPW + chl;
+    return (gch + (cin < a.cpg ? cin : a.cpg - 1)) * S + sl * 4;
+  };
+  auto chain_row = [&](int slab0, int step) {
+    const int cin = slab0 + step * CPW + (tid & 127) / S;
+    return tile * a.d * S + (gch + (cin < a.cpg ? cin : a.cpg - 1)) * S + (tid & 127) % S;
+  };
 
   for (int slab = 0; slab < o.slabs; ++slab) {
     const int slab0 = (cbl * o.slabs + slab) * kSlab;  // first channel of the slab in the group
     if (slab0 >= a.cpg) break;
+    float4 A4 = *reinterpret_cast<const float4*>(a.A + lane_row(slab0, 0));
+    float chained = (tid < 128 ? a.entry : a.exitg)[chain_row(slab0, 0)];
     // prepare: lane = channel, the warp's own tokens
     const bool ch_ok = slab0 + lane < a.cpg;
-    const long long c = (long long)grp * a.cpg + (ch_ok ? slab0 + lane : a.cpg - 1);
+    const long long c = gch + (ch_ok ? slab0 + lane : a.cpg - 1);
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, Dc = a.Dv ? a.Dv[c] : 0.f;
     {
       T rx[kRun], rdt[kRun], rz[kRun], rdy[kRun];
@@ -127,57 +150,61 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
         if (a.z) rz[k] = static_cast<const T*>(a.z)[t * a.zs + c];
       }
 #pragma unroll
-      for (int k = 0; k < kRun; ++k) {
-        const bool ok = ch_ok && tw + k < live;
-        const float delta = softplus_f(to_f32<T>(rdt[k]) + bias);
-        float g = to_f32<T>(rdy[k]);
-        if (a.z) {
-          const float zz = to_f32<T>(rz[k]);
-          g *= zz * fast_sigmoid(zz);
+      for (int k = 0; k < kRun; k += 2) {
+        const float2 d2 = softplus2(make_float2(to_f32<T>(rdt[k]) + bias, to_f32<T>(rdt[k + 1]) + bias));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool ok = ch_ok && tw + k + e < live;
+          const float delta = ok ? (e ? d2.y : d2.x) : 0.f;
+          float g = ok ? to_f32<T>(rdy[k + e]) : 0.f;
+          if (a.z && ok) {
+            const float zz = to_f32<T>(rz[k + e]);
+            g *= zz * fast_sigmoid(zz);
+          }
+          const float u = ok ? delta * to_f32<T>(rx[k + e]) : 0.f;
+          s.du[tw + k + e][lane] = make_float4(delta, delta, u, u);
+          s.dyy[tw + k + e][lane] = make_float2(g, g);
         }
-        s.delta[tw + k][lane] = ok ? delta : 0.f;
-        s.u[tw + k][lane] = ok ? delta * to_f32<T>(rx[k]) : 0.f;
-        s.dyy[tw + k][lane] = ok ? g : 0.f;
       }
     }
     __syncwarp();
 
-    for (int step = 0; step < kSlab / CPW; ++step) {
+    for (int step = 0; step < kSteps; ++step) {
       const int ch = step * CPW + chl;  // channel in the slab
-      const int cin = slab0 + ch;
-      const bool c_ok = cin < a.cpg;
-      const long long crow = ((long long)grp * a.cpg + (c_ok ? cin : a.cpg - 1)) * S + sl * 4;
-      const float4 A4 = *reinterpret_cast<const float4*>(a.A + crow);
-      const float2 A2[2] = {make_float2(A4.x * kLog2eF, A4.y * kLog2eF), make_float2(A4.z * kLog2eF, A4.w * kLog2eF)};
-      // local sweep: decays, end state from zero, gradient sent left with none from the right
+      const bool c_ok = slab0 + ch < a.cpg;
+      const long long crow = lane_row(slab0, step);
+      const float2 A2[2] = {mul2(lo2(A4), dup2(kLog2eF)), mul2(hi2(A4), dup2(kLog2eF))};
       float2 da[kRun][2], hin[kRun][2];
-      {
+      // local sweep: decays, end state from zero, gradient sent left with none from the right
+      auto local_sweep = [&](auto with_edges) {
+        constexpr bool kEdges = decltype(with_edges)::value;
         float2 h0 = dup2(0.f), h1 = dup2(0.f), P0 = dup2(1.f), P1 = dup2(1.f), r0 = dup2(0.f), r1 = dup2(0.f);
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
           const int t = tw + k;
-          const float2 dl = dup2(s.delta[t][ch]), u = dup2(s.u[t][ch]), gy = dup2(s.dyy[t][ch]);
+          const float4 du = s.du[t][ch];
+          const float2 gy = s.dyy[t][ch];
           const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
           const float4 c4 = *reinterpret_cast<const float4*>(&s.C[t][sl * 4]);
-          da[k][0] = decay2(dl, A2[0]);
-          da[k][1] = decay2(dl, A2[1]);
-          if (s.first[t] >= 0) {
+          da[k][0] = decay2(lo2(du), A2[0]);
+          da[k][1] = decay2(lo2(du), A2[1]);
+          if (kEdges && s.first[t] >= 0) {
             h0 = h1 = dup2(0.f);
             if (a.S0) {
               const float4 v = *reinterpret_cast<const float4*>(a.S0 + (long long)s.first[t] * a.d * S + crow);
-              h0 = make_float2(v.x, v.y), h1 = make_float2(v.z, v.w);
+              h0 = lo2(v), h1 = hi2(v);
             }
             P0 = P1 = dup2(0.f);
           }
-          h0 = fma2(da[k][0], h0, mul2(u, make_float2(b4.x, b4.y)));
-          h1 = fma2(da[k][1], h1, mul2(u, make_float2(b4.z, b4.w)));
+          h0 = fma2(da[k][0], h0, mul2(hi2(du), lo2(b4)));
+          h1 = fma2(da[k][1], h1, mul2(hi2(du), hi2(b4)));
           P0 = mul2(P0, da[k][0]);
           P1 = mul2(P1, da[k][1]);
-          float2 g0 = mul2(gy, make_float2(c4.x, c4.y)), g1 = mul2(gy, make_float2(c4.z, c4.w));
-          if (s.last[t] >= 0 && a.dS) {
+          float2 g0 = mul2(gy, lo2(c4)), g1 = mul2(gy, hi2(c4));
+          if (kEdges && s.last[t] >= 0 && a.dS) {
             const float4 v = *reinterpret_cast<const float4*>(a.dS + (long long)s.last[t] * a.d * S + crow);
-            g0 = add2(g0, make_float2(v.x, v.y));
-            g1 = add2(g1, make_float2(v.z, v.w));
+            g0 = add2(g0, lo2(v));
+            g1 = add2(g1, hi2(v));
           }
           r0 = fma2(P0, g0, r0);
           r1 = fma2(P1, g1, r1);
@@ -185,101 +212,108 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
         *reinterpret_cast<float4*>(&s.P[warp][lane * 4]) = make_float4(P0.x, P0.y, P1.x, P1.y);
         *reinterpret_cast<float4*>(&s.H[warp][lane * 4]) = make_float4(h0.x, h0.y, h1.x, h1.y);
         *reinterpret_cast<float4*>(&s.R[warp][lane * 4]) = make_float4(r0.x, r0.y, r1.x, r1.y);
-      }
+      };
+      if (edges) local_sweep(std::true_type{});
+      else local_sweep(std::false_type{});
       __syncthreads();
       // chain the warps: 128 threads forward, 128 in reverse
       {
-        const int i = tid & 127;
-        const int cch = slab0 + step * CPW + i / S;
-        const long long at = tile * a.d * S + ((long long)grp * a.cpg + (cch < a.cpg ? cch : a.cpg - 1)) * S + i % S;
+        const int i = tid & 127, cut = s.cut;
+        float v = chained;
         if (tid < 128) {
-          float h = a.entry[at];
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float loc = s.H[w][i];
-            s.H[w][i] = h;
-            h = s.cut[w] ? loc : fmaf(s.P[w][i], h, loc);
+            const float loc = s.H[w][i], p = s.P[w][i];
+            s.H[w][i] = v;
+            v = (cut >> w) & 1 ? loc : fmaf(p, v, loc);
           }
         } else {
-          float r = a.exitg[at];
 #pragma unroll
           for (int w = kWarps - 1; w >= 0; --w) {
-            const float loc = s.R[w][i];
-            s.R[w][i] = r;
-            r = s.cut[w] ? loc : fmaf(s.P[w][i], r, loc);
+            const float loc = s.R[w][i], p = s.P[w][i];
+            s.R[w][i] = v;
+            v = (cut >> w) & 1 ? loc : fmaf(p, v, loc);
           }
+        }
+        if (step + 1 < kSteps) {
+          A4 = *reinterpret_cast<const float4*>(a.A + lane_row(slab0, step + 1));
+          chained = (tid < 128 ? a.entry : a.exitg)[chain_row(slab0, step + 1)];
+        }
+        // dA of the step before (its own barrier has passed)
+        if (step > 0 && tid < 128) {
+          const int cch = slab0 + (step - 1) * CPW + tid / S;
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) sum += s.dA[(step - 1) & 1][w][tid];
+          if (cch < a.cpg) o.dA_lines[tile * a.d * S + (gch + cch) * S + tid % S] = sum;
         }
       }
       __syncthreads();
-      // the states that enter each token
-      {
-        const float4 v = *reinterpret_cast<const float4*>(&s.H[warp][lane * 4]);
-        float2 h0 = make_float2(v.x, v.y), h1 = make_float2(v.z, v.w);
+      auto final_sweeps = [&](auto with_edges) {
+        constexpr bool kEdges = decltype(with_edges)::value;
+        // the states that enter each token
+        {
+          const float4 v = *reinterpret_cast<const float4*>(&s.H[warp][lane * 4]);
+          float2 h0 = lo2(v), h1 = hi2(v);
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-          const int t = tw + k;
-          if (s.first[t] >= 0) {
-            h0 = h1 = dup2(0.f);
-            if (a.S0) {
-              const float4 q = *reinterpret_cast<const float4*>(a.S0 + (long long)s.first[t] * a.d * S + crow);
-              h0 = make_float2(q.x, q.y), h1 = make_float2(q.z, q.w);
+          for (int k = 0; k < kRun; ++k) {
+            const int t = tw + k;
+            if (kEdges && s.first[t] >= 0) {
+              h0 = h1 = dup2(0.f);
+              if (a.S0) {
+                const float4 q = *reinterpret_cast<const float4*>(a.S0 + (long long)s.first[t] * a.d * S + crow);
+                h0 = lo2(q), h1 = hi2(q);
+              }
+            }
+            hin[k][0] = h0;
+            hin[k][1] = h1;
+            if (k + 1 < kRun) {
+              const float2 u = hi2(s.du[t][ch]);
+              const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
+              h0 = fma2(da[k][0], h0, mul2(u, lo2(b4)));
+              h1 = fma2(da[k][1], h1, mul2(u, hi2(b4)));
             }
           }
-          hin[k][0] = h0;
-          hin[k][1] = h1;
-          if (k + 1 < kRun) {
-            const float2 u = dup2(s.u[t][ch]);
-            const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
-            h0 = fma2(da[k][0], h0, mul2(u, make_float2(b4.x, b4.y)));
-            h1 = fma2(da[k][1], h1, mul2(u, make_float2(b4.z, b4.w)));
-          }
         }
-      }
-      // reverse sweep
-      {
+        // reverse sweep
         const float4 v = *reinterpret_cast<const float4*>(&s.R[warp][lane * 4]);
-        float2 r0 = make_float2(v.x, v.y), r1 = make_float2(v.z, v.w);
-        float2 dA0 = dup2(0.f), dA1 = dup2(0.f);
+        float2 r0 = lo2(v), r1 = hi2(v), dA0 = dup2(0.f), dA1 = dup2(0.f);
 #pragma unroll
         for (int kb = kRun / BT - 1; kb >= 0; --kb) {
           float vA[BT], vG[BT], vY[BT];
 #pragma unroll
           for (int kk = BT - 1; kk >= 0; --kk) {
             const int k = kb * BT + kk, t = tw + k;
-            const float delta = s.delta[t][ch];
-            const float2 u = dup2(s.u[t][ch]), gy = dup2(s.dyy[t][ch]);
+            const float4 du = s.du[t][ch];
+            const float2 gy = s.dyy[t][ch], u = hi2(du);
             const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
             const float4 c4 = *reinterpret_cast<const float4*>(&s.C[t][sl * 4]);
-            const float2 b0 = make_float2(b4.x, b4.y), b1 = make_float2(b4.z, b4.w);
-            const float2 c0 = make_float2(c4.x, c4.y), c1 = make_float2(c4.z, c4.w);
-            if (s.last[t] >= 0) {  // what comes from the right is the final state's gradient
+            if (kEdges && s.last[t] >= 0) {  // what comes from the right is the final state's gradient
               r0 = r1 = dup2(0.f);
               if (a.dS) {
                 const float4 q = *reinterpret_cast<const float4*>(a.dS + (long long)s.last[t] * a.d * S + crow);
-                r0 = make_float2(q.x, q.y), r1 = make_float2(q.z, q.w);
+                r0 = lo2(q), r1 = hi2(q);
               }
             }
-            const float2 g0 = fma2(gy, c0, r0), g1 = fma2(gy, c1, r1);
+            const float2 g0 = fma2(gy, lo2(c4), r0), g1 = fma2(gy, hi2(c4), r1);
             const float2 ah0 = mul2(da[k][0], hin[k][0]), ah1 = mul2(da[k][1], hin[k][1]);
-            const float2 h0 = fma2(u, b0, ah0), h1 = fma2(u, b1, ah1);
-            const float2 gb = fma2(g0, b0, mul2(g1, b1));
+            const float2 h0 = fma2(u, lo2(b4), ah0), h1 = fma2(u, hi2(b4), ah1);
+            const float2 gb = fma2(g0, lo2(b4), mul2(g1, hi2(b4)));
             const float2 ga0 = mul2(g0, ah0), ga1 = mul2(g1, ah1);
-            dA0 = fma2(dup2(delta), ga0, dA0);
-            dA1 = fma2(dup2(delta), ga1, dA1);
+            dA0 = fma2(lo2(du), ga0, dA0);
+            dA1 = fma2(lo2(du), ga1, dA1);
             const float2 sa = fma2(A2[0], ga0, mul2(A2[1], ga1));
-            const float2 yy = fma2(c0, h0, mul2(c1, h1));
+            const float2 yy = fma2(lo2(c4), h0, mul2(hi2(c4), h1));
             vA[kk] = sa.x + sa.y;
             vG[kk] = gb.x + gb.y;
             vY[kk] = yy.x + yy.y;
-            const float2 vb0 = mul2(g0, u), vb1 = mul2(g1, u), vc0 = mul2(gy, h0), vc1 = mul2(gy, h1);
-            float bc[8] = {vb0.x, vb0.y, vb1.x, vb1.y, vc0.x, vc0.y, vc1.x, vc1.y};
-            int at;
-            reduce_scatter<8, CPW, LPC>(bc, lane, &at);
-#pragma unroll
-            for (int j = 0; j < ACC; ++j) acc[k][j] += bc[j];
+            accB[k][0] = fma2(g0, u, accB[k][0]);
+            accB[k][1] = fma2(g1, u, accB[k][1]);
+            accC[k][0] = fma2(gy, h0, accC[k][0]);
+            accC[k][1] = fma2(gy, h1, accC[k][1]);
             r0 = mul2(da[k][0], g0);
             r1 = mul2(da[k][1], g1);
-            if (s.first[t] >= 0 && o.dS0 && c_ok)
+            if (kEdges && s.first[t] >= 0 && o.dS0 && c_ok)
               *reinterpret_cast<float4*>(o.dS0 + (long long)s.first[t] * a.d * S + crow) =
                   make_float4(r0.x, r0.y, r1.x, r1.y);
           }
@@ -294,19 +328,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
             s.yy[t][ch] = vY[0];
           }
         }
-        *reinterpret_cast<float4*>(&s.dA[warp][lane * 4]) = make_float4(dA0.x, dA0.y, dA1.x, dA1.y);
-      }
-      __syncthreads();
-      if (tid < 128) {
-        const int cch = slab0 + step * CPW + tid / S;
-        if (cch < a.cpg) {
-          float v = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) v += s.dA[w][tid];
-          o.dA_lines[tile * a.d * S + ((long long)grp * a.cpg + cch) * S + tid % S] = v;
-        }
-      }
+        *reinterpret_cast<float4*>(&s.dA[step & 1][warp][lane * 4]) = make_float4(dA0.x, dA0.y, dA1.x, dA1.y);
+      };
+      if (edges) final_sweeps(std::true_type{});
+      else final_sweeps(std::false_type{});
     }
+    __syncwarp();
     // outputs per (token, channel): lane = channel, the warp's own tokens
     float dDs = 0.f, dbs = 0.f;
     if (ch_ok) {
@@ -316,7 +343,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
           const long long t = t0 + tw + k;
           const float xv = to_f32<T>(static_cast<const T*>(a.x)[t * a.xs + c]);
           const float raw = to_f32<T>(static_cast<const T*>(a.dt)[t * a.dts + c]) + bias;
-          const float delta = s.delta[tw + k][lane], gy = s.dyy[tw + k][lane], gb = s.gB[tw + k][lane];
+          const float delta = s.du[tw + k][lane].x, gy = s.dyy[tw + k][lane].x, gb = s.gB[tw + k][lane];
           const float ddelta = fmaf(gb, xv, s.sA[tw + k][lane] * kLn2F);
           const float ddt = ddelta * fast_sigmoid(raw);
           static_cast<T*>(o.dx)[t * a.d + c] = from_f32<T>(fmaf(gb, delta, Dc * gy));
@@ -340,30 +367,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kda_selective_scan_bwd_kernel(
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) v += s.ch[w][warp][lane];
-      o.ch_lines[(tile * 2 + warp) * a.d + (long long)grp * a.cpg + slab0 + lane] = v;
+      o.ch_lines[(tile * 2 + warp) * a.d + gch + slab0 + lane] = v;
+    }
+    if (tid >= 128) {  // dA of the slab's last step
+      const int i = tid & 127, cch = slab0 + (kSteps - 1) * CPW + i / S;
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += s.dA[(kSteps - 1) & 1][w][i];
+      if (cch < a.cpg) o.dA_lines[tile * a.d * S + (gch + cch) * S + i % S] = sum;
     }
   }
 
   // dB, dC of the block's channels: [block][token][2][group][S]
-  {
-    int at = 0, have = 8;
+  const bool writer = CPW <= 8 || (chl & 1) == 0;  // CPW 16: two lanes hold each sum
 #pragma unroll
-    for (int b = CPW / 2; b > 0; b >>= 1) {
-      if (have > 1) {
-        have >>= 1;
-        at += (lane & (b * LPC)) ? have : 0;
-      }
+  for (int k = 0; k < kRun; ++k) {
+    float v[8] = {accB[k][0].x, accB[k][0].y, accB[k][1].x, accB[k][1].y,
+                  accC[k][0].x, accC[k][0].y, accC[k][1].x, accC[k][1].y};
+    int at;
+    reduce_scatter<8, CPW, LPC>(v, lane, &at);
+#pragma unroll
+    for (int j = 0; j < ACC; ++j) {
+      const int i = at + j;  // 0..3 dB, 4..7 dC of state sl * 4 + i % 4
+      if (writer && tw + k < live)
+        o.bc_lines[((((long long)cbl * a.q.total + t0 + tw + k) * 2 + i / 4) * o.groups + grp) * S + sl * 4 + i % 4] =
+            v[j];
     }
-    const bool writer = CPW <= 8 || (chl & 1) == 0;  // CPW 16: two lanes hold each sum
-#pragma unroll
-    for (int k = 0; k < kRun; ++k)
-#pragma unroll
-      for (int j = 0; j < ACC; ++j) {
-        const int v = at + j;  // 0..3 dB, 4..7 dC of state sl * 4 + v % 4
-        if (writer && tw + k < live)
-          o.bc_lines[((((long long)cbl * a.q.total + t0 + tw + k) * 2 + v / 4) * o.groups + grp) * S + sl * 4 + v % 4] =
-              acc[k][j];
-      }
   }
 }
 
@@ -398,13 +427,13 @@ struct BwdPlan {
   long long tiles;
   int slabs, blocks_per_group;  // slabs a CTA, CTAs a group and tile
 };
-// Channel blocks: enough CTAs for about eight rounds of two an SM; fewer blocks
+// Channel blocks: enough CTAs for about eight rounds of one an SM; fewer blocks
 // mean fewer lines of dB and dC.
 inline BwdPlan bwd_plan(long long tokens, int d, int groups) {
   BwdPlan p;
   p.tiles = (tokens + kTokens - 1) / kTokens;
   const int all = (d / groups + kSlab - 1) / kSlab;  // slabs a group
-  const long long want = 148 * 16;
+  const long long want = 148 * 8;
   long long per = (want + p.tiles * groups - 1) / (p.tiles > 0 ? p.tiles * groups : 1);
   per = per < 1 ? 1 : per > all ? all : per;
   p.slabs = (int)((all + per - 1) / per);
