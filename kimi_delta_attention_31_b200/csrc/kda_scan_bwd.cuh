@@ -31,6 +31,7 @@ namespace scan {
 constexpr int kRun = 8;                    // tokens a warp
 constexpr int kWarps = 8;
 constexpr int kTokens = kRun * kWarps;     // tokens a tile
+constexpr int kBwdThreads = kWarps * 32;
 constexpr int kSlab = 32;                  // channels prepared at a time
 
 struct BwdOut {
@@ -51,8 +52,9 @@ struct BwdShape {
   static constexpr int BT = LPC < 4 ? LPC : 4;           // tokens whose state sums are exchanged together
 };
 
-template <int S>
+template <typename T, int S>
 struct alignas(16) BwdSmem {
+  T in[2][4][kTokens][kSlab];  // x, dt, dy, z as they are in memory: this slab's and the next one's
   float B[kTokens][S], C[kTokens][S];
   float4 du[kTokens][kSlab];   // delta twice, delta x twice
   float2 dyy[kTokens][kSlab];  // twice
@@ -67,12 +69,12 @@ __device__ __forceinline__ float2 lo2(float4 v) { return make_float2(v.x, v.y); 
 __device__ __forceinline__ float2 hi2(float4 v) { return make_float2(v.z, v.w); }
 
 template <typename T, int S>
-__global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(const Args a, const BwdOut o) {
+__global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(const Args a, const BwdOut o) {
   using Sh = BwdShape<S>;
   constexpr int LPC = Sh::LPC, CPW = Sh::CPW, ACC = Sh::ACC, BT = Sh::BT;
   constexpr int kSteps = kSlab / CPW;  // of a slab
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  BwdSmem<S>& s = *reinterpret_cast<BwdSmem<S>*>(smem_raw);
+  BwdSmem<T, S>& s = *reinterpret_cast<BwdSmem<T, S>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sl = lane % LPC, chl = lane / LPC;
   const int cb = (int)(blockIdx.x % a.ncb);
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
     s.first[tid] = f;
     s.last[tid] = l;
   }
-  for (int e = tid; e < kTokens * S; e += kWarps * 32) {
+  for (int e = tid; e < kTokens * S; e += kBwdThreads) {
     const int t = e / S, k = e % S;
     float b = 0.f, cc = 0.f;
     if (t < live) {
@@ -119,52 +121,79 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
 #pragma unroll
   for (int k = 0; k < kRun; ++k) accB[k][0] = accB[k][1] = accC[k][0] = accC[k][1] = dup2(0.f);
 
-  // first of the four states of this lane in step `step` of the slab at channel slab0 of the group (the last
-  // channel again past the group's end), and of the element that this thread chains
-  auto lane_row = [&](int slab0, int step) {
-    const int cin = slab0 + step * CPW + chl;
-    return (gch + (cin < a.cpg ? cin : a.cpg - 1)) * S + sl * 4;
-  };
+  // Offsets within the group (the last channel again past its end): the lane's four states in step `step` of the slab
+  // at channel slab0, and the element that this thread chains.
+  auto lane_row = [&](int slab0, int step) { return min(slab0 + step * CPW + chl, a.cpg - 1) * S + sl * 4; };
   auto chain_row = [&](int slab0, int step) {
-    const int cin = slab0 + step * CPW + (tid & 127) / S;
-    return tile * a.d * S + (gch + (cin < a.cpg ? cin : a.cpg - 1)) * S + (tid & 127) % S;
+    return min(slab0 + step * CPW + (tid & 127) / S, a.cpg - 1) * S + (tid & 127) % S;
   };
+  const float* Ag = a.A + gch * S;
+  const float* S0g = a.S0 ? a.S0 + gch * S : nullptr;
+  const float* dSg = a.dS ? a.dS + gch * S : nullptr;
+  float* dS0g = o.dS0 ? o.dS0 + gch * S : nullptr;
+  const float* chain_src = (tid < 128 ? a.entry : a.exitg) + (tile * a.d + gch) * S;
+  float* dAg = o.dA_lines + (tile * a.d + gch) * S;
+
+  // the inputs of a slab, by asynchronous copies where their places allow it
+  auto stage_one = [&](T(*dst)[kSlab], const void* src, long long stride, int slab0, int width) {
+    const T* p = static_cast<const T*>(src) + t0 * stride + gch + slab0;
+    if (a.wide) {
+      constexpr int PER = 16 / sizeof(T), N = kSlab / PER;
+#pragma unroll
+      for (int i = 0; i < (kTokens * N + kBwdThreads - 1) / kBwdThreads; ++i) {
+        const int e = i * kBwdThreads + tid, r = e / N, k = (e % N) * PER;
+        if (r < live && k < width) copy_async<16>(&dst[r][k], p + r * stride + k, min(16, (width - k) * (int)sizeof(T)));
+      }
+    } else {
+      for (int r = warp; r < live; r += kWarps)
+        if (lane < width) {
+          if constexpr (sizeof(T) == 4) copy_async<4>(&dst[r][lane], p + r * stride + lane);
+          else dst[r][lane] = p[r * stride + lane];
+        }
+    }
+  };
+  auto stage_slab = [&](int slab) {
+    const int slab0 = (cbl * o.slabs + slab) * kSlab;
+    if (slab < o.slabs && slab0 < a.cpg) {
+      const int width = a.cpg - slab0 < kSlab ? a.cpg - slab0 : kSlab;
+      stage_one(s.in[slab & 1][0], a.x, a.xs, slab0, width);
+      stage_one(s.in[slab & 1][1], a.dt, a.dts, slab0, width);
+      stage_one(s.in[slab & 1][2], a.dy, a.d, slab0, width);
+      if (a.z) stage_one(s.in[slab & 1][3], a.z, a.zs, slab0, width);
+    }
+    copy_async_commit();
+  };
+  stage_slab(0);
 
   for (int slab = 0; slab < o.slabs; ++slab) {
     const int slab0 = (cbl * o.slabs + slab) * kSlab;  // first channel of the slab in the group
     if (slab0 >= a.cpg) break;
-    float4 A4 = *reinterpret_cast<const float4*>(a.A + lane_row(slab0, 0));
-    float chained = (tid < 128 ? a.entry : a.exitg)[chain_row(slab0, 0)];
+    const T(*in)[kTokens][kSlab] = s.in[slab & 1];
+    copy_async_wait<0>();
+    __syncthreads();  // everybody's copies of this slab; the other buffer is free
+    stage_slab(slab + 1);
+    float4 A4 = *reinterpret_cast<const float4*>(Ag + lane_row(slab0, 0));
+    float chained = chain_src[chain_row(slab0, 0)];
     // prepare: lane = channel, the warp's own tokens
     const bool ch_ok = slab0 + lane < a.cpg;
     const long long c = gch + (ch_ok ? slab0 + lane : a.cpg - 1);
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, Dc = a.Dv ? a.Dv[c] : 0.f;
-    {
-      T rx[kRun], rdt[kRun], rz[kRun], rdy[kRun];
 #pragma unroll
-      for (int k = 0; k < kRun; ++k) {
-        const long long t = t0 + (tw + k < live ? tw + k : live - 1);
-        rx[k] = static_cast<const T*>(a.x)[t * a.xs + c];
-        rdt[k] = static_cast<const T*>(a.dt)[t * a.dts + c];
-        rdy[k] = static_cast<const T*>(a.dy)[t * a.d + c];
-        if (a.z) rz[k] = static_cast<const T*>(a.z)[t * a.zs + c];
-      }
+    for (int k = 0; k < kRun; k += 2) {
+      const float2 d2 = softplus2(make_float2(to_f32<T>(in[1][tw + k][lane]) + bias, to_f32<T>(in[1][tw + k + 1][lane]) + bias));
 #pragma unroll
-      for (int k = 0; k < kRun; k += 2) {
-        const float2 d2 = softplus2(make_float2(to_f32<T>(rdt[k]) + bias, to_f32<T>(rdt[k + 1]) + bias));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool ok = ch_ok && tw + k + e < live;
-          const float delta = ok ? (e ? d2.y : d2.x) : 0.f;
-          float g = ok ? to_f32<T>(rdy[k + e]) : 0.f;
-          if (a.z && ok) {
-            const float zz = to_f32<T>(rz[k + e]);
-            g *= zz * fast_sigmoid(zz);
-          }
-          const float u = ok ? delta * to_f32<T>(rx[k + e]) : 0.f;
-          s.du[tw + k + e][lane] = make_float4(delta, delta, u, u);
-          s.dyy[tw + k + e][lane] = make_float2(g, g);
+      for (int e = 0; e < 2; ++e) {
+        const int t = tw + k + e;
+        const bool ok = ch_ok && t < live;  // elsewhere the memory holds anything
+        const float delta = ok ? (e ? d2.y : d2.x) : 0.f;
+        float g = ok ? to_f32<T>(in[2][t][lane]) : 0.f;
+        if (a.z && ok) {
+          const float zz = to_f32<T>(in[3][t][lane]);
+          g *= zz * fast_sigmoid(zz);
         }
+        const float u = ok ? delta * to_f32<T>(in[0][t][lane]) : 0.f;
+        s.du[t][lane] = make_float4(delta, delta, u, u);
+        s.dyy[t][lane] = make_float2(g, g);
       }
     }
     __syncwarp();
@@ -172,7 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
     for (int step = 0; step < kSteps; ++step) {
       const int ch = step * CPW + chl;  // channel in the slab
       const bool c_ok = slab0 + ch < a.cpg;
-      const long long crow = lane_row(slab0, step);
+      const int crow = lane_row(slab0, step);
       const float2 A2[2] = {mul2(lo2(A4), dup2(kLog2eF)), mul2(hi2(A4), dup2(kLog2eF))};
       float2 da[kRun][2], hin[kRun][2];
       // local sweep: decays, end state from zero, gradient sent left with none from the right
@@ -190,8 +219,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
           da[k][1] = decay2(lo2(du), A2[1]);
           if (kEdges && s.first[t] >= 0) {
             h0 = h1 = dup2(0.f);
-            if (a.S0) {
-              const float4 v = *reinterpret_cast<const float4*>(a.S0 + (long long)s.first[t] * a.d * S + crow);
+            if (S0g) {
+              const float4 v = *reinterpret_cast<const float4*>(S0g + (long long)s.first[t] * a.d * S + crow);
               h0 = lo2(v), h1 = hi2(v);
             }
             P0 = P1 = dup2(0.f);
@@ -201,8 +230,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
           P0 = mul2(P0, da[k][0]);
           P1 = mul2(P1, da[k][1]);
           float2 g0 = mul2(gy, lo2(c4)), g1 = mul2(gy, hi2(c4));
-          if (kEdges && s.last[t] >= 0 && a.dS) {
-            const float4 v = *reinterpret_cast<const float4*>(a.dS + (long long)s.last[t] * a.d * S + crow);
+          if (kEdges && s.last[t] >= 0 && dSg) {
+            const float4 v = *reinterpret_cast<const float4*>(dSg + (long long)s.last[t] * a.d * S + crow);
             g0 = add2(g0, lo2(v));
             g1 = add2(g1, hi2(v));
           }
@@ -216,36 +245,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
       if (edges) local_sweep(std::true_type{});
       else local_sweep(std::false_type{});
       __syncthreads();
-      // chain the warps: 128 threads forward, 128 in reverse
+      // chain the warps: 128 threads forward, 128 in reverse; then dA of the step before
       {
         const int i = tid & 127, cut = s.cut;
         float v = chained;
-        if (tid < 128) {
+        float loc[kWarps], p[kWarps];  // in the order of the chain
+        float(*own)[128] = tid < 128 ? s.H : s.R;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float loc = s.H[w][i], p = s.P[w][i];
-            s.H[w][i] = v;
-            v = (cut >> w) & 1 ? loc : fmaf(p, v, loc);
-          }
-        } else {
+        for (int k = 0; k < kWarps; ++k) {
+          const int w = tid < 128 ? k : kWarps - 1 - k;
+          loc[k] = own[w][i];
+          p[k] = (cut >> w) & 1 ? 0.f : s.P[w][i];
+        }
 #pragma unroll
-          for (int w = kWarps - 1; w >= 0; --w) {
-            const float loc = s.R[w][i], p = s.P[w][i];
-            s.R[w][i] = v;
-            v = (cut >> w) & 1 ? loc : fmaf(p, v, loc);
-          }
+        for (int k = 0; k < kWarps; ++k) {
+          const int w = tid < 128 ? k : kWarps - 1 - k;
+          own[w][i] = v;
+          v = p[k] == 0.f ? loc[k] : fmaf(p[k], v, loc[k]);  // nothing passes a start, an infinity neither
         }
         if (step + 1 < kSteps) {
-          A4 = *reinterpret_cast<const float4*>(a.A + lane_row(slab0, step + 1));
-          chained = (tid < 128 ? a.entry : a.exitg)[chain_row(slab0, step + 1)];
+          A4 = *reinterpret_cast<const float4*>(Ag + lane_row(slab0, step + 1));
+          chained = chain_src[chain_row(slab0, step + 1)];
         }
-        // dA of the step before (its own barrier has passed)
-        if (step > 0 && tid < 128) {
-          const int cch = slab0 + (step - 1) * CPW + tid / S;
+        if (step > 0 && tid >= kBwdThreads - 128) {
+          const int cch = slab0 + (step - 1) * CPW + i / S;
           float sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) sum += s.dA[(step - 1) & 1][w][tid];
-          if (cch < a.cpg) o.dA_lines[tile * a.d * S + (gch + cch) * S + tid % S] = sum;
+          for (int w = 0; w < kWarps; ++w) sum += s.dA[(step - 1) & 1][w][i];
+          if (cch < a.cpg) dAg[cch * S + i % S] = sum;
         }
       }
       __syncthreads();
@@ -260,8 +287,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
             const int t = tw + k;
             if (kEdges && s.first[t] >= 0) {
               h0 = h1 = dup2(0.f);
-              if (a.S0) {
-                const float4 q = *reinterpret_cast<const float4*>(a.S0 + (long long)s.first[t] * a.d * S + crow);
+              if (S0g) {
+                const float4 q = *reinterpret_cast<const float4*>(S0g + (long long)s.first[t] * a.d * S + crow);
                 h0 = lo2(q), h1 = hi2(q);
               }
             }
@@ -290,8 +317,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
             const float4 c4 = *reinterpret_cast<const float4*>(&s.C[t][sl * 4]);
             if (kEdges && s.last[t] >= 0) {  // what comes from the right is the final state's gradient
               r0 = r1 = dup2(0.f);
-              if (a.dS) {
-                const float4 q = *reinterpret_cast<const float4*>(a.dS + (long long)s.last[t] * a.d * S + crow);
+              if (dSg) {
+                const float4 q = *reinterpret_cast<const float4*>(dSg + (long long)s.last[t] * a.d * S + crow);
                 r0 = lo2(q), r1 = hi2(q);
               }
             }
@@ -313,8 +340,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
             accC[k][1] = fma2(gy, h1, accC[k][1]);
             r0 = mul2(da[k][0], g0);
             r1 = mul2(da[k][1], g1);
-            if (kEdges && s.first[t] >= 0 && o.dS0 && c_ok)
-              *reinterpret_cast<float4*>(o.dS0 + (long long)s.first[t] * a.d * S + crow) =
+            if (kEdges && s.first[t] >= 0 && dS0g && c_ok)
+              *reinterpret_cast<float4*>(dS0g + (long long)s.first[t] * a.d * S + crow) =
                   make_float4(r0.x, r0.y, r1.x, r1.y);
           }
           int at;
@@ -341,8 +368,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
       for (int k = 0; k < kRun; ++k) {
         if (tw + k < live) {
           const long long t = t0 + tw + k;
-          const float xv = to_f32<T>(static_cast<const T*>(a.x)[t * a.xs + c]);
-          const float raw = to_f32<T>(static_cast<const T*>(a.dt)[t * a.dts + c]) + bias;
+          const float xv = to_f32<T>(in[0][tw + k][lane]);
+          const float raw = to_f32<T>(in[1][tw + k][lane]) + bias;
           const float delta = s.du[tw + k][lane].x, gy = s.dyy[tw + k][lane].x, gb = s.gB[tw + k][lane];
           const float ddelta = fmaf(gb, xv, s.sA[tw + k][lane] * kLn2F);
           const float ddt = ddelta * fast_sigmoid(raw);
@@ -351,8 +378,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
           dDs = fmaf(gy, xv, dDs);
           dbs += ddt;
           if (a.z) {
-            const float zz = to_f32<T>(static_cast<const T*>(a.z)[t * a.zs + c]);
-            const float dyo = to_f32<T>(static_cast<const T*>(a.dy)[t * a.d + c]);
+            const float zz = to_f32<T>(in[3][tw + k][lane]);
+            const float dyo = to_f32<T>(in[2][tw + k][lane]);
             const float sg = fast_sigmoid(zz);
             const float y = fmaf(Dc, xv, s.yy[tw + k][lane]);
             static_cast<T*>(o.dz)[t * a.d + c] = from_f32<T>(dyo * y * sg * fmaf(zz, 1.f - sg, 1.f));
@@ -369,12 +396,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kda_selective_scan_bwd_kernel(
       for (int w = 0; w < kWarps; ++w) v += s.ch[w][warp][lane];
       o.ch_lines[(tile * 2 + warp) * a.d + gch + slab0 + lane] = v;
     }
-    if (tid >= 128) {  // dA of the slab's last step
+    if (tid >= 128 && tid < 256) {  // dA of the slab's last step
       const int i = tid & 127, cch = slab0 + (kSteps - 1) * CPW + i / S;
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += s.dA[(kSteps - 1) & 1][w][i];
-      if (cch < a.cpg) o.dA_lines[tile * a.d * S + (gch + cch) * S + i % S] = sum;
+      if (cch < a.cpg) dAg[cch * S + i % S] = sum;
     }
   }
 
@@ -486,17 +513,18 @@ cudaError_t launch_bwd(Args a, BwdOut o, float* dA, float* dB, float* dC, float*
     a.blocks_per_group = a.ncb / groups;
     if ((e = launch_scan<T, S, kLocalBwd>(a, st)) != cudaSuccess) return e;
     if ((e = launch_carry(a, S, true, st)) != cudaSuccess) return e;
+    a.wide = wide_copies(a, (int)sizeof(T));
     a.ncb = p.blocks_per_group * groups;
     a.blocks_per_group = p.blocks_per_group;
     static PerDeviceOnce once;
     e = run_once_per_device(once, [] {
       return cudaFuncSetAttribute(kda_selective_scan_bwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)sizeof(BwdSmem<S>));
+                                  (int)sizeof(BwdSmem<T, S>));
     });
     if (e != cudaSuccess) return e;
     const long long grid = p.tiles * a.ncb;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kda_selective_scan_bwd_kernel<T, S><<<(unsigned)grid, kWarps * 32, sizeof(BwdSmem<S>), st>>>(a, o);
+    kda_selective_scan_bwd_kernel<T, S><<<(unsigned)grid, kBwdThreads, sizeof(BwdSmem<T, S>), st>>>(a, o);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long bc = tokens * 2 * groups * S;
     kda_scan_sum_bc_kernel<<<(unsigned)((bc + 255) / 256), 256, 0, st>>>(o.bc_lines, dB, dC, p.blocks_per_group,
