@@ -28,7 +28,7 @@
 namespace kda {
 namespace scan {
 
-constexpr int kRun = 8;                    // tokens a warp
+constexpr int kRun = 8;                    // tokens a warp (6 tokens and 12 warps: 8% slower; 4 and 16: 9%)
 constexpr int kWarps = 8;
 constexpr int kTokens = kRun * kWarps;     // tokens a tile
 constexpr int kBwdThreads = kWarps * 32;
@@ -164,6 +164,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
     copy_async_commit();
   };
   stage_slab(0);
+  // of the step to come
+  float4 A4 = *reinterpret_cast<const float4*>(Ag + lane_row(cbl * o.slabs * kSlab, 0));
+  float chained = chain_src[chain_row(cbl * o.slabs * kSlab, 0)];
 
   for (int slab = 0; slab < o.slabs; ++slab) {
     const int slab0 = (cbl * o.slabs + slab) * kSlab;  // first channel of the slab in the group
@@ -172,8 +175,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
     copy_async_wait<0>();
     __syncthreads();  // everybody's copies of this slab; the other buffer is free
     stage_slab(slab + 1);
-    float4 A4 = *reinterpret_cast<const float4*>(Ag + lane_row(slab0, 0));
-    float chained = chain_src[chain_row(slab0, 0)];
     // prepare: lane = channel, the warp's own tokens
     const bool ch_ok = slab0 + lane < a.cpg;
     const long long c = gch + (ch_ok ? slab0 + lane : a.cpg - 1);
@@ -263,10 +264,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
           own[w][i] = v;
           v = p[k] == 0.f ? loc[k] : fmaf(p[k], v, loc[k]);  // nothing passes a start, an infinity neither
         }
-        if (step + 1 < kSteps) {
-          A4 = *reinterpret_cast<const float4*>(Ag + lane_row(slab0, step + 1));
-          chained = chain_src[chain_row(slab0, step + 1)];
-        }
+        // (the next slab's first step follows the last one; past the block it is read and not used)
+        A4 = *reinterpret_cast<const float4*>(Ag + lane_row(slab0, step + 1));
+        chained = chain_src[chain_row(slab0, step + 1)];
         if (step > 0 && tid >= kBwdThreads - 128) {
           const int cch = slab0 + (step - 1) * CPW + i / S;
           float sum = 0.f;
