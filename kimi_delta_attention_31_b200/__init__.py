@@ -705,39 +705,26 @@ def _row_stride(name, t, inner=1):
     return step
 
 
-def _check_dense(device, tensors):
-    """The (name, tensor or None) pairs are contiguous, on the CUDA device `device`."""
-    if device.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device")
-    for name, t in tensors:
+def _check_tensors(dev, tensors, strided=0):
+    """Each (name, tensor or None, dtype, shape): its type and shape, its
+    device's index, and, but for the first `strided`, that it is contiguous."""
+    for name, t, dtype, shape in tensors:
         if t is not None:
-            if not t.is_contiguous():
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+            if strided <= 0 and not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-            if t.device != device:
-                raise ValueError(f"tensors on different devices ({device} and {name} on {t.device})")
-
-
-def _check_rows(device, dense, rows):
-    """Checks `dense` as _check_dense does; ``rows`` = (name, tensor, inner
-    dimensions) may have evenly spaced rows: returns their strides."""
-    strides = [0 if t is None else _row_stride(name, t, inner) for name, t, inner in rows]
-    _check_dense(device, dense)
-    for name, t, _ in rows:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on different devices ({device} and {name} on {t.device})")
-    return strides
-
-
-def _expect(name, t, dtype, shape):
-    if t is None:
-        return
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+            if t.get_device() != dev:
+                raise ValueError(f"tensors on different devices (index {dev}, {name} on {t.device})")
+        strided -= 1
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
 
 
 _ACT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+_F32 = torch.float32
 
 
 def _act_code(name, t):
@@ -754,13 +741,16 @@ def _addr(t):
 _SAME_DEVICE = contextlib.nullcontext()
 
 
-def _on(device):
-    """The device made current for the call (nothing to do where it is)."""
-    return _SAME_DEVICE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _on(dev):
+    """Device `dev` made current for the call (nothing to do where it is)."""
+    return _SAME_DEVICE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _dense_like(x):
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _new_workspace(need, workspace, device):
@@ -773,17 +763,11 @@ def _new_workspace(need, workspace, device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _norm_args(x, weight, residual, s):
-    code = _act_code("x", x)
+def _norm_dim(x):
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"x must be [..., D], got {tuple(x.shape)}")
     D = x.shape[-1]
-    wcode = _act_code("weight", weight)
-    if weight.shape != (D,):
-        raise ValueError(f"weight must be {(D,)}, got {tuple(weight.shape)}")
-    _expect("residual", residual, x.dtype, x.shape)
-    _expect("s", s, x.dtype, x.shape)
-    return D, x.numel() // D, code, wcode
+    return D, x.numel() // D
 
 
 def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=None, s=None):
@@ -793,16 +777,19 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=None, s=None):
     bf16 or fp32; residual: as x, or None.  Returns (y, s) in x's dtype, s None
     without a residual.  y may be x and s may be residual."""
     lib = _lib or load_library()
-    D, rows, code, wcode = _norm_args(x, weight, residual, s)
-    _expect("y", y, x.dtype, x.shape)
-    (xs,) = _check_rows(x.device, [("weight", weight), ("residual", residual), ("y", y), ("s", s)], [("x", x, 1)])
-    with _on(x.device):
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
+    code, wcode, dev, shape, dtype = _act_code("x", x), _act_code("weight", weight), x.get_device(), x.shape, x.dtype
+    D, rows = _norm_dim(x)
+    xs = _row_stride("x", x)
+    _check_tensors(dev, (("weight", weight, weight.dtype, (D,)), ("residual", residual, dtype, shape),
+                         ("y", y, dtype, shape), ("s", s, dtype, shape)))
+    with _on(dev):
+        y = _dense_like(x) if y is None else y
         if s is None and residual is not None:
-            s = torch.empty_like(x, memory_format=torch.contiguous_format)
-        st = lib.kda_rms_norm_fwd(_addr(x), xs, _addr(residual), _addr(weight), wcode, _addr(y), _addr(s),
-                                  rows, D, eps, code, _raw_stream(x.device))
-    _check(st)
+            s = _dense_like(x)
+        st = lib.kda_rms_norm_fwd(x.data_ptr(), xs, _addr(residual), weight.data_ptr(), wcode, y.data_ptr(), _addr(s),
+                                  rows, D, eps, code, _raw_stream(dev))
+    if st:
+        _check(st)
     return y, s
 
 
@@ -811,20 +798,22 @@ def rms_norm_quant_fwd(x, weight, residual=None, eps=1e-6, group=0, s=None):
     each group of `group` columns (32, 64 or 128; 0: the whole row), q = y /
     scale.  Returns (q [..., D] float8_e4m3fn, scale [..., D / group] fp32, s)."""
     lib = _lib or load_library()
-    D, rows, code, wcode = _norm_args(x, weight, residual, s)
-    group = int(group)
+    code, wcode, dev, shape, dtype = _act_code("x", x), _act_code("weight", weight), x.get_device(), x.shape, x.dtype
+    D, rows = _norm_dim(x)
     if group < 0 or (group and D % group):
         raise ValueError(f"group={group} must be 0 or divide D={D}")
-    (xs,) = _check_rows(x.device, [("weight", weight), ("residual", residual), ("s", s)], [("x", x, 1)])
-    with _on(x.device):
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scale = torch.empty((*x.shape[:-1], D // group if group else 1), dtype=torch.float32, device=x.device)
+    xs = _row_stride("x", x)
+    _check_tensors(dev, (("weight", weight, weight.dtype, (D,)), ("residual", residual, dtype, shape),
+                         ("s", s, dtype, shape)))
+    with _on(dev):
+        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty((*shape[:-1], D // group if group else 1), dtype=_F32, device=x.device)
         if s is None and residual is not None:
-            s = torch.empty_like(x, memory_format=torch.contiguous_format)
-        st = lib.kda_rms_norm_quant_fwd(_addr(x), xs, _addr(residual), _addr(weight), wcode, _addr(q),
-                                        _addr(scale), _addr(s), rows, D, group, eps, code,
-                                        _raw_stream(x.device))
-    _check(st)
+            s = _dense_like(x)
+        st = lib.kda_rms_norm_quant_fwd(x.data_ptr(), xs, _addr(residual), weight.data_ptr(), wcode, q.data_ptr(),
+                                        scale.data_ptr(), _addr(s), rows, D, group, eps, code, _raw_stream(dev))
+    if st:
+        _check(st)
     return q, scale, s
 
 
@@ -834,18 +823,18 @@ def rms_norm_bwd(dy, s, weight, ds=None, eps=1e-6, dx=None, workspace=None):
     Returns a dict: dx (the gradient of x and of residual, ds included; may be
     dy or ds) and dweight [D] fp32."""
     lib = _lib or load_library()
-    D, rows, code, wcode = _norm_args(s, weight, None, dx)
-    _expect("dy", dy, s.dtype, s.shape)
-    _expect("ds", ds, s.dtype, s.shape)
-    _check_dense(s.device, (("dy", dy), ("s", s), ("weight", weight), ("ds", ds), ("dx", dx)))
-    with _on(s.device):
+    code, wcode, dev, shape, dtype = _act_code("s", s), _act_code("weight", weight), s.get_device(), s.shape, s.dtype
+    D, rows = _norm_dim(s)
+    _check_tensors(dev, (("s", s, dtype, shape), ("dy", dy, dtype, shape), ("weight", weight, weight.dtype, (D,)),
+                         ("ds", ds, dtype, shape), ("dx", dx, dtype, shape)))
+    with _on(dev):
         dx = torch.empty_like(s) if dx is None else dx
-        dweight = torch.empty(D, dtype=torch.float32, device=s.device)
-        workspace, ws_bytes = _new_workspace(int(lib.kda_rms_norm_bwd_workspace_size(rows, D)), workspace, s.device)
-        st = lib.kda_rms_norm_bwd(_addr(dy), _addr(s), _addr(weight), wcode, _addr(ds), _addr(dx),
-                                  _addr(dweight), rows, D, eps, code, _addr(workspace), ws_bytes,
-                                  _raw_stream(s.device))
-    _check(st)
+        dweight = torch.empty(D, dtype=_F32, device=s.device)
+        workspace, ws_bytes = _new_workspace(lib.kda_rms_norm_bwd_workspace_size(rows, D), workspace, s.device)
+        st = lib.kda_rms_norm_bwd(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), wcode, _addr(ds), dx.data_ptr(),
+                                  dweight.data_ptr(), rows, D, eps, code, _addr(workspace), ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st)
     return dict(dx=dx, dweight=dweight)
 
 
@@ -862,41 +851,40 @@ def _sequences(x, cu_seqlens):
     return B, T, n, n
 
 
-def _conv_args(x, weight, bias):
-    code = _act_code("x", x)
+def _conv_dim(x, weight, dims):
+    if x.dim() != dims:
+        raise ValueError(f"x must be {'[B,T,D]' if dims == 3 else '[N,D]'}, got {tuple(x.shape)}")
     D = x.shape[-1]
     if weight.dim() != 2 or weight.shape[0] != D or not 2 <= weight.shape[1] <= 4:
         raise ValueError(f"weight must be [D={D}, W] with W 2, 3 or 4, got {tuple(weight.shape)}")
-    wcode = _act_code("weight", weight)
-    _expect("bias", bias, weight.dtype, (D,))
-    return D, weight.shape[1], code, wcode
+    return D, weight.shape[1]
 
 
 def short_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, output_final_state=True, y=None,
                    state_out=None):
     """Short causal depthwise convolution with SiLU: x [B,T,D] (a slice of a
-    joint projection may be given), weight [D,W] with W 2 to 4, bias [D] or None,
-    state [N,W-1,D] or None (the inputs before each sequence), cu_seqlens int32
-    [N+1] (B == 1) or None.  Returns (y [B,T,D], state_out [N,W-1,D], None when
-    output_final_state is False)."""
+    joint projection may be given), weight [D,W] with W 2 to 4, bias [D] in
+    weight's dtype or None, state [N,W-1,D] or None (the inputs before each
+    sequence), cu_seqlens int32 [N+1] (B == 1) or None.  Returns (y [B,T,D],
+    state_out [N,W-1,D], None when output_final_state is False)."""
     lib = _lib or load_library()
-    if x.dim() != 3:
-        raise ValueError(f"x must be [B,T,D], got {tuple(x.shape)}")
-    D, W, code, wcode = _conv_args(x, weight, bias)
+    code, wcode, dev, dtype, wdtype = _act_code("x", x), _act_code("weight", weight), x.get_device(), x.dtype, weight.dtype
+    D, W = _conv_dim(x, weight, 3)
     B, T, num_seqs, N = _sequences(x, cu_seqlens)
-    _expect("state", state, x.dtype, (N, W - 1, D))
-    _expect("state_out", state_out, x.dtype, (N, W - 1, D))
-    _expect("y", y, x.dtype, x.shape)
-    (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("cu_seqlens", cu_seqlens),
-                                   ("y", y), ("state_out", state_out)], [("x", x, 1)])
-    with _on(x.device):
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
+    xs = _row_stride("x", x)
+    kept = (N, W - 1, D)
+    _check_tensors(dev, (("weight", weight, wdtype, weight.shape), ("bias", bias, wdtype, (D,)),
+                         ("state", state, dtype, kept), ("state_out", state_out, dtype, kept), ("y", y, dtype, x.shape),
+                         ("cu_seqlens", cu_seqlens, torch.int32, (num_seqs + 1,))))
+    with _on(dev):
+        y = _dense_like(x) if y is None else y
         if state_out is None and output_final_state:
-            state_out = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
-        st = lib.kda_short_conv_fwd(_addr(x), xs, _addr(weight), _addr(bias), wcode, _addr(state), _addr(y),
-                                    _addr(state_out), _addr(cu_seqlens), num_seqs, B, T, D, W, code,
-                                    _raw_stream(x.device))
-    _check(st)
+            state_out = torch.empty(kept, dtype=dtype, device=x.device)
+        st = lib.kda_short_conv_fwd(x.data_ptr(), xs, weight.data_ptr(), _addr(bias), wcode, _addr(state),
+                                    y.data_ptr(), _addr(state_out), _addr(cu_seqlens), num_seqs, B, T, D, W, code,
+                                    _raw_stream(dev))
+    if st:
+        _check(st)
     return y, state_out
 
 
@@ -904,21 +892,20 @@ def short_conv_step(x, weight, state, bias=None, state_out=None, y=None):
     """One token per sequence: x [N,D], state [N,W-1,D], updated in place unless
     state_out is given.  Returns y [N,D]."""
     lib = _lib or load_library()
-    if x.dim() != 2:
-        raise ValueError(f"x must be [N,D], got {tuple(x.shape)}")
-    D, W, code, wcode = _conv_args(x, weight, bias)
+    code, wcode, dev, dtype, wdtype = _act_code("x", x), _act_code("weight", weight), x.get_device(), x.dtype, weight.dtype
+    D, W = _conv_dim(x, weight, 2)
     N = x.shape[0]
-    _expect("state", state, x.dtype, (N, W - 1, D))
-    _expect("state_out", state_out, x.dtype, (N, W - 1, D))
-    _expect("y", y, x.dtype, x.shape)
-    (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("y", y),
-                                   ("state_out", state_out)], [("x", x, 1)])
-    with _on(x.device):
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
-        st = lib.kda_short_conv_step(_addr(x), xs, _addr(weight), _addr(bias), wcode, _addr(state), _addr(y),
-                                     _addr(state if state_out is None else state_out), N, D, W, code,
-                                     _raw_stream(x.device))
-    _check(st)
+    xs = _row_stride("x", x)
+    kept = (N, W - 1, D)
+    _check_tensors(dev, (("weight", weight, wdtype, weight.shape), ("bias", bias, wdtype, (D,)),
+                         ("state", state, dtype, kept), ("state_out", state_out, dtype, kept), ("y", y, dtype, x.shape)))
+    with _on(dev):
+        y = _dense_like(x) if y is None else y
+        st = lib.kda_short_conv_step(x.data_ptr(), xs, weight.data_ptr(), _addr(bias), wcode, state.data_ptr(),
+                                     y.data_ptr(), (state if state_out is None else state_out).data_ptr(), N, D, W, code,
+                                     _raw_stream(dev))
+    if st:
+        _check(st)
     return y
 
 
@@ -928,57 +915,54 @@ def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, cu_seqlens
     x's dtype, dweight [D,W], dbias [D] (None without a bias) and dinit [N,W-1,D]
     (the gradient of state), fp32."""
     lib = _lib or load_library()
-    if x.dim() != 3:
-        raise ValueError(f"x must be [B,T,D], got {tuple(x.shape)}")
-    D, W, code, wcode = _conv_args(x, weight, bias)
+    code, wcode, dev, dtype, wdtype = _act_code("x", x), _act_code("weight", weight), x.get_device(), x.dtype, weight.dtype
+    D, W = _conv_dim(x, weight, 3)
     B, T, num_seqs, N = _sequences(x, cu_seqlens)
-    if dy.dtype is not torch.float32:
-        _expect("dy", dy, x.dtype, x.shape)
-    _expect("dy", dy, dy.dtype, x.shape)
-    _expect("state", state, x.dtype, (N, W - 1, D))
-    _expect("dstate", dstate, torch.float32, (N, W - 1, D))
-    (xs,) = _check_rows(x.device, [("weight", weight), ("bias", bias), ("state", state), ("cu_seqlens", cu_seqlens),
-                                   ("dy", dy), ("dstate", dstate)], [("x", x, 1)])
-    f32 = dict(dtype=torch.float32, device=x.device)
-    with _on(x.device):
-        out = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format), dweight=torch.empty((D, W), **f32),
-                   dbias=None if bias is None else torch.empty(D, **f32), dinit=torch.empty((N, W - 1, D), **f32))
-        workspace, ws_bytes = _new_workspace(int(lib.kda_short_conv_bwd_workspace_size(B, T, D, W)), workspace, x.device)
-        st = lib.kda_short_conv_bwd(_addr(x), xs, _addr(weight), _addr(bias), wcode, _addr(state), _addr(dy),
-                                    _ACT[dy.dtype], _addr(dstate), _addr(out["dx"]), _addr(out["dweight"]),
-                                    _addr(out["dbias"]), _addr(out["dinit"]), _addr(cu_seqlens), num_seqs, B, T, D, W,
-                                    code, _addr(workspace), ws_bytes, _raw_stream(x.device))
-    _check(st)
+    xs = _row_stride("x", x)
+    kept = (N, W - 1, D)
+    _check_tensors(dev, (("weight", weight, wdtype, weight.shape), ("bias", bias, wdtype, (D,)),
+                         ("state", state, dtype, kept), ("dstate", dstate, _F32, kept),
+                         ("dy", dy, dtype if dy.dtype is not _F32 else _F32, x.shape),
+                         ("cu_seqlens", cu_seqlens, torch.int32, (num_seqs + 1,))))
+    with _on(dev):
+        f32 = dict(dtype=_F32, device=x.device)
+        out = dict(dx=_dense_like(x), dweight=torch.empty((D, W), **f32),
+                   dbias=None if bias is None else torch.empty(D, **f32), dinit=torch.empty(kept, **f32))
+        workspace, ws_bytes = _new_workspace(lib.kda_short_conv_bwd_workspace_size(B, T, D, W), workspace, x.device)
+        st = lib.kda_short_conv_bwd(x.data_ptr(), xs, weight.data_ptr(), _addr(bias), wcode, _addr(state),
+                                    dy.data_ptr(), _ACT[dy.dtype], _addr(dstate), out["dx"].data_ptr(),
+                                    out["dweight"].data_ptr(), _addr(out["dbias"]), out["dinit"].data_ptr(),
+                                    _addr(cu_seqlens), num_seqs, B, T, D, W, code, _addr(workspace), ws_bytes,
+                                    _raw_stream(dev))
+    if st:
+        _check(st)
     return out
 
 
-def _scan_args(x, dt, A, B, C, D, z, dt_bias, lead):
-    code = _act_code("x", x)
-    if x.dim() != lead + 1:
-        raise ValueError(f"x must have {lead + 1} dimensions, got {tuple(x.shape)}")
-    d = x.shape[-1]
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dims, more):
+    """Checks a scan's inputs ([B,T,..] with dims 3, [N,..] with dims 2) and the
+    tensors of `more`.  Returns (sizes d, S, groups, dtype code, arguments of the
+    C ABI up to the state)."""
+    code, dev, dtype = _act_code("x", x), x.get_device(), x.dtype
+    if x.dim() != dims:
+        raise ValueError(f"x must have {dims} dimensions, got {tuple(x.shape)}")
+    shape = x.shape
+    d = shape[-1]
     if A.dim() != 2 or A.shape[0] != d:
         raise ValueError(f"A must be [d={d}, S], got {tuple(A.shape)}")
-    S = A.shape[1]
-    _expect("A", A, torch.float32, A.shape)
-    _expect("dt", dt, x.dtype, x.shape)
-    _expect("z", z, x.dtype, x.shape)
-    if B.dim() != lead + 2:
+    if B.dim() != dims + 1:
         raise ValueError(f"B must be [..., groups, S], got {tuple(B.shape)}")
-    groups = B.shape[-2]
+    S, groups = A.shape[1], B.shape[-2]
     if groups < 1 or d % groups:
         raise ValueError(f"the groups of B and C ({groups}) must divide d={d}")
-    for name, t in (("B", B), ("C", C)):
-        _expect(name, t, x.dtype, (*x.shape[:-1], groups, S))
-    _expect("D", D, torch.float32, (d,))
-    _expect("dt_bias", dt_bias, torch.float32, (d,))
-    return d, S, groups, code
-
-
-def _scan_ptrs(x, dt, A, B, C, D, z, dt_bias, state, strides):
-    xs, dts, zs, bs, cs = strides
-    return (_addr(x), xs, _addr(dt), dts, _addr(A), _addr(B), bs, _addr(C), cs, _addr(D), _addr(z), zs, _addr(dt_bias),
-            _addr(state))
+    bc = (*shape[:-1], groups, S)
+    _check_tensors(dev, (("x", x, dtype, shape), ("dt", dt, dtype, shape), ("z", z, dtype, shape), ("B", B, dtype, bc),
+                         ("C", C, dtype, bc), ("A", A, _F32, A.shape), ("D", D, _F32, (d,)),
+                         ("dt_bias", dt_bias, _F32, (d,)), *more), 5)
+    args = (x.data_ptr(), _row_stride("x", x), dt.data_ptr(), _row_stride("dt", dt), A.data_ptr(), B.data_ptr(),
+            _row_stride("B", B, 2), C.data_ptr(), _row_stride("C", C, 2), _addr(D), _addr(z),
+            0 if z is None else _row_stride("z", z), _addr(dt_bias))
+    return d, S, groups, code, args
 
 
 def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu_seqlens=None,
@@ -991,24 +975,24 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu
     slices of a joint projection.  Returns (y [B,T,d], S_out [N,d,S] fp32, None
     when output_final_state is False)."""
     lib = _lib or load_library()
-    d, S, groups, code = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B,T,d], got {tuple(x.shape)}")
     nb, T, num_seqs, N = _sequences(x, cu_seqlens)
-    _expect("S0", S0, torch.float32, (N, d, S))
-    _expect("S_out", S_out, torch.float32, (N, d, S))
-    _expect("y", y, x.dtype, x.shape)
-    strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S0", S0), ("cu_seqlens", cu_seqlens),
-                                     ("y", y), ("S_out", S_out)],
-                          [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
-    with _on(x.device):
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
+    kept = (N, *A.shape)
+    d, S, groups, code, args = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, 3, (
+        ("S0", S0, _F32, kept), ("S_out", S_out, _F32, kept), ("y", y, x.dtype, x.shape),
+        ("cu_seqlens", cu_seqlens, torch.int32, (num_seqs + 1,))))
+    dev = x.get_device()
+    with _on(dev):
+        y = _dense_like(x) if y is None else y
         if S_out is None and output_final_state:
-            S_out = torch.empty((N, d, S), dtype=torch.float32, device=x.device)
-        need = int(lib.kda_selective_scan_fwd_workspace_size(nb, T, d, S, groups, num_seqs))
+            S_out = torch.empty(kept, dtype=_F32, device=x.device)
+        need = lib.kda_selective_scan_fwd_workspace_size(nb, T, d, S, groups, num_seqs)
         workspace, ws_bytes = _new_workspace(need, workspace, x.device)
-        st = lib.kda_selective_scan_fwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _addr(y), _addr(S_out),
-                                        _addr(cu_seqlens), num_seqs, nb, T, d, S, groups, code,
-                                        _addr(workspace), ws_bytes, _raw_stream(x.device))
-    _check(st)
+        st = lib.kda_selective_scan_fwd(*args, _addr(S0), y.data_ptr(), _addr(S_out), _addr(cu_seqlens), num_seqs, nb, T,
+                                        d, S, groups, code, _addr(workspace), ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st)
     return y, S_out
 
 
@@ -1016,19 +1000,16 @@ def selective_scan_step(x, dt, A, B, C, S, D=None, z=None, dt_bias=None, S_out=N
     """One token per sequence: x, dt, z [N,d]; B, C [N,groups,S]; the state S
     [N,d,S] fp32 is updated in place unless S_out is given.  Returns y [N,d]."""
     lib = _lib or load_library()
-    d, ns, groups, code = _scan_args(x, dt, A, B, C, D, z, dt_bias, 1)
-    N = x.shape[0]
-    _expect("S", S, torch.float32, (N, d, ns))
-    _expect("S_out", S_out, torch.float32, (N, d, ns))
-    _expect("y", y, x.dtype, x.shape)
-    strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S", S), ("S_out", S_out), ("y", y)],
-                          [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
-    with _on(x.device):
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
-        st = lib.kda_selective_scan_step(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S, strides), _addr(y),
-                                         _addr(S if S_out is None else S_out), N, d, ns, groups, code,
-                                         _raw_stream(x.device))
-    _check(st)
+    kept = (x.shape[0], *A.shape)
+    d, ns, groups, code, args = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, 2, (
+        ("S", S, _F32, kept), ("S_out", S_out, _F32, kept), ("y", y, x.dtype, x.shape)))
+    dev = x.get_device()
+    with _on(dev):
+        y = _dense_like(x) if y is None else y
+        st = lib.kda_selective_scan_step(*args, S.data_ptr(), y.data_ptr(), (S if S_out is None else S_out).data_ptr(),
+                                         kept[0], d, ns, groups, code, _raw_stream(dev))
+    if st:
+        _check(st)
     return y
 
 
@@ -1039,29 +1020,29 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, S0=None
     x's dtype (dz None without z) and, fp32, dA [d,S], dB, dC [B,T,groups,S], dD,
     ddt_bias [d] (None without D, dt_bias) and dS0 [N,d,S]."""
     lib = _lib or load_library()
-    d, S, groups, code = _scan_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B,T,d], got {tuple(x.shape)}")
     nb, T, num_seqs, N = _sequences(x, cu_seqlens)
-    _expect("dy", dy, x.dtype, x.shape)
-    _expect("S0", S0, torch.float32, (N, d, S))
-    _expect("dS", dS, torch.float32, (N, d, S))
-    strides = _check_rows(x.device, [("A", A), ("D", D), ("dt_bias", dt_bias), ("S0", S0), ("dS", dS), ("dy", dy),
-                                     ("cu_seqlens", cu_seqlens)],
-                          [("x", x, 1), ("dt", dt, 1), ("z", z, 1), ("B", B, 2), ("C", C, 2)])
-    f32 = dict(dtype=torch.float32, device=x.device)
-    with _on(x.device):
-        out = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format), ddt=torch.empty_like(x, memory_format=torch.contiguous_format),
-                   dz=None if z is None else torch.empty_like(x, memory_format=torch.contiguous_format), dA=torch.empty((d, S), **f32),
-                   dB=torch.empty(B.shape, **f32), dC=torch.empty(B.shape, **f32),
+    kept = (N, *A.shape)
+    d, S, groups, code, args = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, 3, (
+        ("dy", dy, x.dtype, x.shape), ("S0", S0, _F32, kept), ("dS", dS, _F32, kept),
+        ("cu_seqlens", cu_seqlens, torch.int32, (num_seqs + 1,))))
+    dev = x.get_device()
+    with _on(dev):
+        f32 = dict(dtype=_F32, device=x.device)
+        out = dict(dx=_dense_like(x), ddt=_dense_like(x), dz=None if z is None else _dense_like(x),
+                   dA=torch.empty((d, S), **f32), dB=torch.empty(B.shape, **f32), dC=torch.empty(B.shape, **f32),
                    dD=None if D is None else torch.empty(d, **f32),
-                   ddt_bias=None if dt_bias is None else torch.empty(d, **f32), dS0=torch.empty((N, d, S), **f32))
-        need = int(lib.kda_selective_scan_bwd_workspace_size(nb, T, d, S, groups))
+                   ddt_bias=None if dt_bias is None else torch.empty(d, **f32), dS0=torch.empty(kept, **f32))
+        need = lib.kda_selective_scan_bwd_workspace_size(nb, T, d, S, groups)
         workspace, ws_bytes = _new_workspace(need, workspace, x.device)
-        st = lib.kda_selective_scan_bwd(*_scan_ptrs(x, dt, A, B, C, D, z, dt_bias, S0, strides), _addr(dy), _addr(dS),
-                                        _addr(out["dx"]), _addr(out["ddt"]), _addr(out["dA"]), _addr(out["dB"]),
-                                        _addr(out["dC"]), _addr(out["dD"]), _addr(out["dz"]), _addr(out["ddt_bias"]),
-                                        _addr(out["dS0"]), _addr(cu_seqlens), num_seqs, nb, T, d, S, groups,
-                                        code, _addr(workspace), ws_bytes, _raw_stream(x.device))
-    _check(st)
+        st = lib.kda_selective_scan_bwd(*args, _addr(S0), dy.data_ptr(), _addr(dS), out["dx"].data_ptr(),
+                                        out["ddt"].data_ptr(), out["dA"].data_ptr(), out["dB"].data_ptr(),
+                                        out["dC"].data_ptr(), _addr(out["dD"]), _addr(out["dz"]),
+                                        _addr(out["ddt_bias"]), out["dS0"].data_ptr(), _addr(cu_seqlens), num_seqs, nb,
+                                        T, d, S, groups, code, _addr(workspace), ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st)
     return out
 
 

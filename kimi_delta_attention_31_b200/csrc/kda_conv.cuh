@@ -11,17 +11,76 @@
 //
 // A thread owns VEC channels and walks a run of L tokens with the window in
 // registers, so every input is read once but for the W-1 rows before each run
-// (which the run before reads too: L2).  HBM-bound; a group of U tokens is
-// loaded while the one before it is computed.  Products and sums are fp32, the
-// output is rounded once.
+// (which the run before reads too: L2).  HBM-bound: tokens arrive by asynchronous
+// copies in groups of kGroup, a few groups ahead, in a ring in shared memory that
+// each thread has to itself (no barrier; loads ahead in registers left too few
+// threads on an SM: 316 us for 65536 tokens of 4096 channels, 52% of the copy
+// rate).  Products and sums are fp32, two at a time; the output is rounded once.
 #pragma once
+#include <type_traits>
+
 #include "kda_layer_common.cuh"
 
 namespace kda {
 namespace conv {
 
 constexpr int kThreads = 128;
-constexpr int kGroup = 4;  // tokens loaded ahead
+constexpr int kGroup = 4;  // tokens of a group
+
+// One thread's tokens [t0, t1) of one input, `stride` elements apart, GROUPS - 1
+// groups ahead.  Threads with one element a token load them in order instead.
+template <typename T, int VEC, int GROUPS>
+struct Feed {
+  Pack<T, VEC> (*ring)[kThreads];
+  const T* p;
+  long long stride, t1, next;
+  int slot;
+  __device__ __forceinline__ Feed(Pack<T, VEC> (*r)[kThreads], const T* src, long long st, long long t0, long long end)
+      : ring(r), p(src + t0 * st), stride(st), t1(end), next(t0), slot(0) {}
+  __device__ __forceinline__ void stage() {  // the next group; its slots were read a group ago
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      if (next + i < t1) copy_async<sizeof(T) * VEC>(&ring[slot * kGroup + i][threadIdx.x], p + i * stride);
+    copy_async_commit();
+    p += kGroup * stride;
+    next += kGroup;
+    slot = slot + 1 < GROUPS ? slot + 1 : 0;
+  }
+};
+template <typename T, int VEC, int GROUPS>
+__device__ __forceinline__ void read_group(const Feed<T, VEC, GROUPS>& f, int slot, int i, float (&out)[VEC]) {
+  unpack<T, VEC>(f.ring[slot * kGroup + i][threadIdx.x], out);
+}
+// silu of the sums p, and (backward) its slope: silu' = sg + p sg (1 - sg).
+template <int VEC>
+__device__ __forceinline__ void sigmoids(const float (&p)[VEC], float (&sg)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sg[e] = fast_sigmoid(p[e]);
+}
+// acc += x y
+template <int VEC>
+__device__ __forceinline__ void add_product(float (&acc)[VEC], const float (&x)[VEC], const float (&y)[VEC]) {
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 v = fma2(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]), make_float2(acc[e], acc[e + 1]));
+      acc[e] = v.x;
+      acc[e + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = fmaf(x[e], y[e], acc[e]);
+  }
+}
+// p = b + sum_j w_j rows[j]
+template <int VEC, int W>
+__device__ __forceinline__ void window_sum(const float (&wt)[W][VEC], const float (&b)[VEC], const float (*rows)[VEC],
+                                           float (&p)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) p[e] = b[e];
+#pragma unroll
+  for (int j = 0; j < W; ++j) add_product<VEC>(p, wt[j], rows[j]);
+}
 
 struct FwdArgs {
   const void* x;
@@ -86,9 +145,12 @@ __device__ __forceinline__ void load_window(const void* x, long long x_stride, c
   }
 }
 
+constexpr int kFwdGroups = 4;  // groups in the forward's ring
+
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) kda_short_conv_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kda_short_conv_fwd_kernel(const FwdArgs a) {
   constexpr int U = kGroup;
+  __shared__ Pack<T, VEC> s_ring[VEC > 1 ? kFwdGroups * U : 1][kThreads];
   const int col = (int)(blockIdx.x % a.ncol);
   const long long run = blockIdx.x / a.ncol;
   const int c0 = (col * kThreads + (int)threadIdx.x) * VEC;
@@ -110,51 +172,68 @@ __global__ void __launch_bounds__(kThreads) kda_short_conv_fwd_kernel(const FwdA
   const long long t1 = t0 + a.L < a.q.total ? t0 + a.L : a.q.total;
   if (t0 >= t1) return;
 
+  const T* xp = static_cast<const T*>(a.x) + c0;
+  Feed<T, VEC, kFwdGroups> feed(s_ring, xp, a.x_stride, t0, t1);
+  if constexpr (VEC > 1) {
+#pragma unroll
+    for (int g = 0; g < kFwdGroups - 1; ++g) feed.stage();
+  }
   float wt[W][VEC], b[VEC];
   load_weights<VEC, W>(a.w, a.bias, a.w_bf16, c0, wt, b);
   int n = seq_of_token(a.q, t0);
   long long end = seq_end(a.q, n);
   float xs[U + W - 1][VEC];
   load_window<T, VEC, W>(a.x, a.x_stride, a.state, n, seq_start(a.q, n), t0, a.D, c0, xs);
-
-  const T* xp = static_cast<const T*>(a.x) + c0;
-  T* yp = static_cast<T*>(a.y) + c0;
-  Pack<T, VEC> next[U];
-#pragma unroll
-  for (int i = 0; i < U; ++i)
-    if (t0 + i < t1) next[i] = load_pack<T, VEC>(xp + (t0 + i) * a.x_stride);
-  for (long long t = t0; t < t1; t += U) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) unpack<T, VEC>(next[i], xs[W - 1 + i]);
+  T* yp = static_cast<T*>(a.y) + t0 * a.D + c0;
+  Pack<T, VEC> next[VEC > 1 ? 1 : U];
+  if constexpr (VEC == 1) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (t + U + i < t1) next[i] = load_pack<T, VEC>(xp + (t + U + i) * a.x_stride);
+      if (t0 + i < t1) next[VEC > 1 ? 0 : i] = load_pack<T, VEC>(xp + (t0 + i) * a.x_stride);
+  }
+  int slot = 0;
+  for (long long t = t0; t < t1; t += U) {
+    if constexpr (VEC > 1) {
+      feed.stage();
+      copy_async_wait<kFwdGroups - 1>();
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const long long ti = t + i;
-      if (ti < t1) {
-        if (ti == end) {  // the first token of another sequence
-          n = seq_of_token(a.q, ti);
-          end = seq_end(a.q, n);
+      for (int i = 0; i < U; ++i) read_group(feed, slot, i, xs[W - 1 + i]);
+      slot = slot + 1 < kFwdGroups ? slot + 1 : 0;
+    } else {
 #pragma unroll
-          for (int r = 0; r < W - 1; ++r) load_state_row<T, VEC, W>(a.state, n, r, a.D, c0, xs[i + r]);
-        }
-        float y[VEC];
+      for (int i = 0; i < U; ++i) unpack<T, VEC>(next[VEC > 1 ? 0 : i], xs[W - 1 + i]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float p = b[e];
+      for (int i = 0; i < U; ++i)
+        if (t + U + i < t1) next[VEC > 1 ? 0 : i] = load_pack<T, VEC>(xp + (t + U + i) * a.x_stride);
+    }
+    auto tokens = [&](auto plain) {  // plain: U tokens inside one sequence, which ends later
 #pragma unroll
-          for (int j = 0; j < W; ++j) p = fmaf(wt[j][e], xs[i + j][e], p);
-          y[e] = p * fast_sigmoid(p);
-        }
-        store_pack<T, VEC>(yp + ti * a.D, y);
-        if (ti + 1 == end && state_out) {
+      for (int i = 0; i < U; ++i) {
+        const long long ti = t + i;
+        if (decltype(plain)::value || ti < t1) {
+          if (!decltype(plain)::value && ti == end) {  // the first token of another sequence
+            n = seq_of_token(a.q, ti);
+            end = seq_end(a.q, n);
 #pragma unroll
-          for (int r = 0; r < W - 1; ++r)
-            store_pack<T, VEC>(state_out + ((long long)n * (W - 1) + r) * a.D + c0, xs[i + 1 + r]);
+            for (int r = 0; r < W - 1; ++r) load_state_row<T, VEC, W>(a.state, n, r, a.D, c0, xs[i + r]);
+          }
+          float p[VEC], sg[VEC];
+          window_sum<VEC, W>(wt, b, xs + i, p);
+          sigmoids<VEC>(p, sg);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) p[e] *= sg[e];
+          store_pack<T, VEC>(yp + (long long)i * a.D, p);
+          if (!decltype(plain)::value && ti + 1 == end && state_out) {
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r)
+              store_pack<T, VEC>(state_out + ((long long)n * (W - 1) + r) * a.D + c0, xs[i + 1 + r]);
+          }
         }
       }
-    }
+    };
+    if (t + U <= t1 && (end > t + U || end < t)) tokens(std::true_type{});
+    else tokens(std::false_type{});
+    yp += (long long)U * a.D;
 #pragma unroll
     for (int r = 0; r < W - 1; ++r)
 #pragma unroll
@@ -215,9 +294,13 @@ struct BwdArgs {
   long long L;
 };
 
+constexpr int kBwdGroups = 3;  // groups in the backward's rings
+
 template <typename T, typename TDY, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) kda_short_conv_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kda_short_conv_bwd_kernel(const BwdArgs a) {
   constexpr int U = kGroup;
+  __shared__ Pack<T, VEC> s_x[VEC > 1 ? kBwdGroups * U : 1][kThreads];
+  __shared__ Pack<TDY, VEC> s_dy[VEC > 1 ? kBwdGroups * U : 1][kThreads];
   const int col = (int)(blockIdx.x % a.ncol);
   const long long run = blockIdx.x / a.ncol;
   const int c0 = (col * kThreads + (int)threadIdx.x) * VEC;
@@ -256,88 +339,104 @@ __global__ void __launch_bounds__(kThreads) kda_short_conv_bwd_kernel(const BwdA
 #pragma unroll
       for (int e = 0; e < VEC; ++e) dps[r][e] = 0.f;
 
-    Pack<T, VEC> nx[U];
-    Pack<TDY, VEC> ny[U];
+    Feed<T, VEC, kBwdGroups> fx(s_x, xp, a.x_stride, tb, t1);
+    Feed<TDY, VEC, kBwdGroups> fy(s_dy, dyp, a.D, tb, t1);
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (tb + i < t1) {
-        nx[i] = load_pack<T, VEC>(xp + (tb + i) * a.x_stride);
-        ny[i] = load_pack<TDY, VEC>(dyp + (tb + i) * a.D);
-      }
-    for (long long t = tb; t < t1; t += U) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        unpack<T, VEC>(nx[i], xs[W - 1 + i]);
-        unpack<TDY, VEC>(ny[i], dps[W - 1 + i]);
-      }
+      for (int g = 0; g < kBwdGroups - 1; ++g) fx.stage(), fy.stage();
+    }
+    int slot = 0;
+    Pack<T, VEC> nx[VEC > 1 ? 1 : U];
+    Pack<TDY, VEC> ny[VEC > 1 ? 1 : U];
+    if constexpr (VEC == 1) {
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        if (t + U + i < t1) {
-          nx[i] = load_pack<T, VEC>(xp + (t + U + i) * a.x_stride);
-          ny[i] = load_pack<TDY, VEC>(dyp + (t + U + i) * a.D);
+        if (tb + i < t1) {
+          nx[VEC > 1 ? 0 : i] = load_pack<T, VEC>(xp + (tb + i) * a.x_stride);
+          ny[VEC > 1 ? 0 : i] = load_pack<TDY, VEC>(dyp + (tb + i) * a.D);
+        }
+    }
+    for (long long t = tb; t < t1; t += U) {
+      if constexpr (VEC > 1) {
+        fx.stage();
+        fy.stage();
+        copy_async_wait<2 * (kBwdGroups - 1)>();  // x and dy are committed in turn
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          read_group(fx, slot, i, xs[W - 1 + i]);
+          read_group(fy, slot, i, dps[W - 1 + i]);
+        }
+        slot = slot + 1 < kBwdGroups ? slot + 1 : 0;
+      } else {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          unpack<T, VEC>(nx[VEC > 1 ? 0 : i], xs[W - 1 + i]);
+          unpack<TDY, VEC>(ny[VEC > 1 ? 0 : i], dps[W - 1 + i]);
         }
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const long long ti = t + i;
-        if (ti < t1) {
-          if (ti == end) {
-            n = seq_of_token(a.q, ti);
-            start = seq_start(a.q, n);
-            end = seq_end(a.q, n);
-#pragma unroll
-            for (int r = 0; r < W - 1; ++r) {
-              load_state_row<T, VEC, W>(a.state, n, r, a.D, c0, xs[i + r]);
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) dps[i + r][e] = 0.f;
-            }
+        for (int i = 0; i < U; ++i)
+          if (t + U + i < t1) {
+            nx[VEC > 1 ? 0 : i] = load_pack<T, VEC>(xp + (t + U + i) * a.x_stride);
+            ny[VEC > 1 ? 0 : i] = load_pack<TDY, VEC>(dyp + (t + U + i) * a.D);
           }
-          const bool own = ti >= t0;
-          float drow[VEC];
+      }
+      auto tokens = [&](auto plain) {  // plain: U own tokens inside one sequence, past its first W-1, which ends later
+        constexpr bool kPlain = decltype(plain)::value;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float p = b[e];
+        for (int i = 0; i < U; ++i) {
+          const long long ti = t + i;
+          if (kPlain || ti < t1) {
+            if (!kPlain && ti == end) {
+              n = seq_of_token(a.q, ti);
+              start = seq_start(a.q, n);
+              end = seq_end(a.q, n);
 #pragma unroll
-            for (int j = 0; j < W; ++j) p = fmaf(wt[j][e], xs[i + j][e], p);
-            const float sg = fast_sigmoid(p);
-            const float dp = dps[i + W - 1][e] * fmaf(p * sg, 1.f - sg, sg);
-            dps[i + W - 1][e] = dp;
+              for (int r = 0; r < W - 1; ++r) {
+                load_state_row<T, VEC, W>(a.state, n, r, a.D, c0, xs[i + r]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) dps[i + r][e] = 0.f;
+              }
+            }
+            const bool own = kPlain || ti >= t0;
+            float p[VEC], sg[VEC], drow[VEC] = {};
+            window_sum<VEC, W>(wt, b, xs + i, p);
+            sigmoids<VEC>(p, sg);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dps[i + W - 1][e] *= fmaf(p[e] * sg[e], 1.f - sg[e], sg[e]);
             if (own) {
 #pragma unroll
-              for (int j = 0; j < W; ++j) dw[j][e] = fmaf(dp, xs[i + j][e], dw[j][e]);
-              db[e] += dp;
-            }
-            float d = 0.f;
+              for (int j = 0; j < W; ++j) add_product<VEC>(dw[j], dps[i + W - 1], xs[i + j]);
 #pragma unroll
-            for (int j = 0; j < W; ++j) d = fmaf(wt[j][e], dps[i + W - 1 - j][e], d);
-            drow[e] = d;
-          }
-          if (own) {
-            const long long r = ti - start;  // the row finished here, counted from the state's first
-            if (r >= W - 1) {
-              if (ti >= W - 1) store_pack<T, VEC>(dxp + (ti - (W - 1)) * a.D, drow);
-            } else if (a.dinit && r >= 0) {
-              store_floats<VEC>(a.dinit + ((long long)n * (W - 1) + r) * a.D + c0, drow);
-            }
-            if (ti + 1 == end) {  // the rows that only the tokens up to here, and the state out, see
+              for (int e = 0; e < VEC; ++e) db[e] += dps[i + W - 1][e];
 #pragma unroll
-              for (int k = 0; k < W - 1; ++k) {
-                float tail[VEC] = {};
-                if (a.dstate) load_floats<VEC>(a.dstate + ((long long)n * (W - 1) + k) * a.D + c0, tail);
+              for (int j = 0; j < W; ++j) add_product<VEC>(drow, wt[j], dps[i + W - 1 - j]);
+              const long long r = ti - start;  // the row finished here, counted from the state's first
+              if (kPlain || r >= W - 1) {
+                if (kPlain || ti >= W - 1) store_pack<T, VEC>(dxp + (ti - (W - 1)) * a.D, drow);
+              } else if (a.dinit && r >= 0) {
+                store_floats<VEC>(a.dinit + ((long long)n * (W - 1) + r) * a.D + c0, drow);
+              }
+              if (!kPlain && ti + 1 == end) {  // the rows that only the tokens up to here, and the state out, see
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
+                for (int k = 0; k < W - 1; ++k) {
+                  float tail[VEC] = {};
+                  if (a.dstate) load_floats<VEC>(a.dstate + ((long long)n * (W - 1) + k) * a.D + c0, tail);
 #pragma unroll
-                  for (int j = k + 1; j < W; ++j) tail[e] = fmaf(wt[j][e], dps[i + W + k - j][e], tail[e]);
-                const long long rk = r + 1 + k;
-                if (rk >= W - 1) {
-                  if (ti + 1 + k >= W - 1) store_pack<T, VEC>(dxp + (ti + 1 + k - (W - 1)) * a.D, tail);
-                } else if (a.dinit && rk >= 0) {
-                  store_floats<VEC>(a.dinit + ((long long)n * (W - 1) + rk) * a.D + c0, tail);
+                  for (int j = k + 1; j < W; ++j) add_product<VEC>(tail, wt[j], dps[i + W + k - j]);
+                  const long long rk = r + 1 + k;
+                  if (rk >= W - 1) {
+                    if (ti + 1 + k >= W - 1) store_pack<T, VEC>(dxp + (ti + 1 + k - (W - 1)) * a.D, tail);
+                  } else if (a.dinit && rk >= 0) {
+                    store_floats<VEC>(a.dinit + ((long long)n * (W - 1) + rk) * a.D + c0, tail);
+                  }
                 }
               }
             }
           }
         }
-      }
+      };
+      if (t >= t0 && t + U <= t1 && t >= W - 1 && t - start >= W - 1 && end > t + U) tokens(std::true_type{});
+      else tokens(std::false_type{});
 #pragma unroll
       for (int r = 0; r < W - 1; ++r)
 #pragma unroll

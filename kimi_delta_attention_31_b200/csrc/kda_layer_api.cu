@@ -117,12 +117,12 @@ kda_status_t norm_fwd_impl(const char* fn, int quant, const void* x, long long x
                     aligned(weight, weight_dtype == KDA_F32 ? 16u : 2u * vec);
   if (quant == kda::norm::kGroup && !wide)
     return misaligned(fn, "group scales need 16-byte aligned rows and pointers");
-  kda::norm::FwdArgs a{x, x_stride, residual, weight, weight_dtype == KDA_BF16, y, scale, s, rows, D, group, eps, 0, 1};
+  kda::norm::FwdArgs a{x, x_stride, residual, weight, weight_dtype == KDA_BF16, y, scale, s, rows, D, group, eps, 1, 1};
   cudaError_t e = cudaErrorInvalidValue;
 #define KDA_NORM_CASE(TYPE, V)                                                                        \
   e = quant == kda::norm::kNone  ? kda::norm::launch_fwd<TYPE, V, kda::norm::kNone>(a, stream)         \
       : quant == kda::norm::kRow ? kda::norm::launch_fwd<TYPE, V, kda::norm::kRow>(a, stream)          \
-                                 : kda::norm::launch_fwd<TYPE, V, kda::norm::kGroup>(a, stream)
+                                 : kda::norm::launch_fwd_groups<TYPE, V>(a, stream)
   if (dtype == KDA_BF16 && wide) KDA_NORM_CASE(__nv_bfloat16, 8);
   else if (dtype == KDA_F32 && wide) KDA_NORM_CASE(float, 4);
 #undef KDA_NORM_CASE

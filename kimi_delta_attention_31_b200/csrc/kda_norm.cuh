@@ -23,7 +23,9 @@ namespace norm {
 constexpr float kFp8Max = 448.f;
 constexpr float kScaleFloor = 1e-10f;
 constexpr int kMaxDim = 16384;
-enum QuantMode : int { kNone = 0, kRow = 1, kGroup = 2 };
+// What is stored: T, e4m3 with a scale a row, or with a scale a group of columns
+// (the mode is then the lanes of one group, 4 to 32).
+enum QuantMode : int { kNone = 0, kRow = 1, kGroup = 4 };
 
 struct FwdArgs {
   const void* x;
@@ -37,7 +39,8 @@ struct FwdArgs {
   long long rows;
   int D, group;
   float eps;
-  int group_lanes_log2, groups;  // kGroup: lanes of one group (2^.., at most 32), groups a row
+  int groups;      // scales a row
+  int turns;       // rows a thread takes one after the other (RU at a time)
 };
 
 // Sum (or maximum) of NVAL values each over the TPR threads of a row; every
@@ -96,121 +99,132 @@ constexpr int threads_of(int tpr) { return tpr <= 32 ? 128 : tpr; }  // a row of
 constexpr int rows_at_once(int tpr, int nv) { return tpr <= 32 && nv == 1 ? 2 : 1; }
 
 template <typename T, int VEC, int TPR, int NV, int QUANT>
-__global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 ? 8 : 1) kda_rms_norm_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 && NV == 1 ? 7 : 1)
+    kda_rms_norm_fwd_kernel(const FwdArgs a) {
   constexpr int NT = threads_of(TPR);
   constexpr int RPC = NT / TPR;  // row slots of a CTA
   constexpr int RU = rows_at_once(TPR, NV);
+  constexpr bool kAhead = TPR <= 32 && NV == 1;  // several turns, the next one's rows loaded during one
+  constexpr int GL = QUANT >= kGroup ? QUANT : 1;  // lanes of one group
   __shared__ float s_red[2][RU][32];
   const int j = threadIdx.x % TPR;
-  const long long row0 = ((long long)blockIdx.x * RPC + threadIdx.x / TPR) * RU;
   const int nvec = a.D / VEC;
-  const T* xp = static_cast<const T*>(a.x);
-  const T* rp = static_cast<const T*>(a.residual);
+  const T* xp = static_cast<const T*>(a.x) + j * VEC;
+  const T* rp = a.residual ? static_cast<const T*>(a.residual) + j * VEC : nullptr;
+  const int turns = kAhead ? a.turns : 1;
+  long long row0 = ((long long)blockIdx.x * turns * RPC + threadIdx.x / TPR) * RU;
+  const long long step = (long long)RPC * RU;
 
   Pack<T, VEC> px[RU][NV], pr[RU][NV];
-  float v[RU][NV][VEC];
-#pragma unroll
-  for (int u = 0; u < RU; ++u) {
-    const long long row = row0 + u < a.rows ? row0 + u : a.rows - 1;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = j + i * TPR;
-      if (c < nvec) {
-        px[u][i] = load_pack<T, VEC>(xp + row * a.x_stride + (long long)c * VEC);
-        if (rp) pr[u][i] = load_pack<T, VEC>(rp + row * a.D + (long long)c * VEC);
-      }
-    }
-  }
-  float w[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (j + i * TPR < nvec) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, w[i]);
-  float acc[RU];
-  const float inv_d = 1.f / (float)a.D;
-#pragma unroll
-  for (int u = 0; u < RU; ++u) {
-    acc[u] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (j + i * TPR < nvec) {
-        unpack<T, VEC>(px[u][i], v[u][i]);
-        if (rp) {
-          float q[VEC];
-          unpack<T, VEC>(pr[u][i], q);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v[u][i][e] += q[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[u][i][e] = w[i][e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[u] = fmaf(v[u][i][e], v[u][i][e], acc[u]);
-    }
-  }
-  if (a.s) {
-#pragma unroll
-    for (int u = 0; u < RU; ++u)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = j + i * TPR;
-        if (row0 + u < a.rows && c < nvec)
-          store_pack<T, VEC>(static_cast<T*>(a.s) + (row0 + u) * a.D + (long long)c * VEC, v[u][i]);
-      }
-  }
-  // the sum is taken of the unrounded s (the stored s is rounded once, to T)
-  row_reduce<TPR, false>(acc, s_red[0]);
-  float amax[RU];
-#pragma unroll
-  for (int u = 0; u < RU; ++u) {
-    const float r = rsqrtf(acc[u] * inv_d + a.eps);
-    amax[u] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        v[u][i][e] = v[u][i][e] * r * w[i][e];
-        if (QUANT == kRow) amax[u] = max_nan(amax[u], fabsf(v[u][i][e]));
-      }
-  }
-  if constexpr (QUANT == kNone) {
-#pragma unroll
-    for (int u = 0; u < RU; ++u)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = j + i * TPR;
-        if (row0 + u < a.rows && c < nvec)
-          store_pack<T, VEC>(static_cast<T*>(a.y) + (row0 + u) * a.D + (long long)c * VEC, v[u][i]);
-      }
-  } else {
-    if constexpr (QUANT == kRow) row_reduce<TPR, true>(amax, s_red[1]);
-    const int gl = 1 << a.group_lanes_log2;
+  auto fetch = [&](long long first) {
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
-      const bool live = row0 + u < a.rows;
+      const long long row = first + u < a.rows ? first + u : a.rows - 1;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (j + i * TPR < nvec) {
+          px[u][i] = load_pack<T, VEC>(xp + row * a.x_stride + i * TPR * VEC);
+          if (rp) pr[u][i] = load_pack<T, VEC>(rp + row * a.D + i * TPR * VEC);
+        }
+    }
+  };
+  fetch(row0);
+  float w[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (j + i * TPR < nvec) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, w[i]);
+    else
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[i][e] = 0.f;
+  }
+  const float inv_d = 1.f / (float)a.D;
+#pragma unroll 1
+  for (int turn = 0; turn < turns; ++turn, row0 += step) {
+    if (RPC > 1 && row0 - threadIdx.x / TPR * RU >= a.rows) return;  // (uniform: a CTA's slots are consecutive rows)
+    float v[RU][NV][VEC], acc[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      acc[u] = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = j + i * TPR;
-        float m = amax[u];
-        if constexpr (QUANT == kGroup) {
-          m = 0.f;
+        if (j + i * TPR < nvec) {
+          unpack<T, VEC>(px[u][i], v[u][i]);
+          if (rp) {
+            float q[VEC];
+            unpack<T, VEC>(pr[u][i], q);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) m = max_nan(m, fabsf(v[u][i][e]));
+            for (int e = 0; e < VEC; ++e) v[u][i][e] += q[e];
+          }
+        } else {
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1)
-            if (o < gl) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+          for (int e = 0; e < VEC; ++e) v[u][i][e] = 0.f;
         }
-        m = max_nan(m, kScaleFloor);
-        const bool first = QUANT == kGroup ? (c & (gl - 1)) == 0 : c == 0;
-        if (live && c < nvec && first)
-          a.scale[(row0 + u) * a.groups + (QUANT == kGroup ? c >> a.group_lanes_log2 : 0)] = m / kFp8Max;
-        // 448 / m: the reciprocal's argument scaled down, so that a huge m does not flush it to 0
-        const float inv = fast_rcp(m * 0x1p-10f) * (kFp8Max * 0x1p-10f);
-        if (live && c < nvec) {
-          float q[VEC];
+      }
+    }
+    if (kAhead && turn + 1 < turns) fetch(row0 + step);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) q[e] = v[u][i][e] * inv;
-          store_fp8<VEC>(static_cast<uint8_t*>(a.y) + (row0 + u) * a.D + (long long)c * VEC, q);
+    for (int u = 0; u < RU; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[u] = fmaf(v[u][i][e], v[u][i][e], acc[u]);
+    if (a.s) {
+#pragma unroll
+      for (int u = 0; u < RU; ++u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (row0 + u < a.rows && j + i * TPR < nvec)
+            store_pack<T, VEC>(static_cast<T*>(a.s) + (row0 + u) * a.D + (j + i * TPR) * VEC, v[u][i]);
+    }
+    // the sum is taken of the unrounded s (the stored s is rounded once, to T)
+    row_reduce<TPR, false>(acc, s_red[0]);
+    float amax[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      const float r = rsqrtf(acc[u] * inv_d + a.eps);
+      amax[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          v[u][i][e] = v[u][i][e] * r * w[i][e];
+          if (QUANT == kRow) amax[u] = max_nan(amax[u], fabsf(v[u][i][e]));
+        }
+    }
+    if constexpr (QUANT == kNone) {
+#pragma unroll
+      for (int u = 0; u < RU; ++u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (row0 + u < a.rows && j + i * TPR < nvec)
+            store_pack<T, VEC>(static_cast<T*>(a.y) + (row0 + u) * a.D + (j + i * TPR) * VEC, v[u][i]);
+    } else {
+      if constexpr (QUANT == kRow) row_reduce<TPR, true>(amax, s_red[1]);
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        const bool live = row0 + u < a.rows;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = j + i * TPR;
+          float m = amax[u];
+          if constexpr (QUANT >= kGroup) {
+            m = 0.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) m = max_nan(m, fabsf(v[u][i][e]));
+#pragma unroll
+            for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+          }
+          m = max_nan(m, kScaleFloor);
+          if (live && c < nvec && (QUANT >= kGroup ? c % GL == 0 : c == 0))
+            a.scale[(row0 + u) * a.groups + (QUANT >= kGroup ? c / GL : 0)] = m / kFp8Max;
+          // 448 / m: the reciprocal's argument scaled down, so that a huge m does not flush it to 0
+          const float inv = fast_rcp(m * 0x1p-10f) * (kFp8Max * 0x1p-10f);
+          if (live && c < nvec) {
+            float q[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) q[e] = v[u][i][e] * inv;
+            store_fp8<VEC>(static_cast<uint8_t*>(a.y) + (row0 + u) * a.D + c * VEC, q);
+          }
         }
       }
     }
@@ -376,23 +390,40 @@ inline RowShape row_shape_bwd(int vecs) {
 #define KDA_NORM_SHAPES_LONG(CASE) CASE(512, 8)
 #define KDA_NORM_SHAPES_SCALAR(CASE) CASE(512, 16) CASE(512, 32)
 
+// Turns of the forward's small rows: the set-up of a thread is worth several
+// rows, as long as every SM keeps about 32 CTAs' worth of them.
+inline int fwd_turns(long long rows, int rows_a_turn) {
+  const long long t = rows / ((long long)rows_a_turn * 148 * 32);
+  return (int)(t < 1 ? 1 : t > 8 ? 8 : t);
+}
+
 template <typename T, int VEC, int QUANT>
 cudaError_t launch_fwd(FwdArgs a, cudaStream_t st) {
   const RowShape sh = row_shape(a.D / VEC);
-  a.group_lanes_log2 = 0;
-  a.groups = QUANT == kGroup ? a.D / a.group : 1;
-  if (QUANT == kGroup)
-    while ((VEC << a.group_lanes_log2) < a.group) ++a.group_lanes_log2;
+  a.groups = QUANT >= kGroup ? a.D / a.group : 1;
 #define KDA_CASE(TPR, NV)                                                                               \
   if (sh.tpr == TPR && sh.nv == NV) {                                                                    \
     constexpr int NT = threads_of(TPR), RPC = NT / TPR * rows_at_once(TPR, NV);                           \
-    kda_rms_norm_fwd_kernel<T, VEC, TPR, NV, QUANT><<<(unsigned)((a.rows + RPC - 1) / RPC), NT, 0, st>>>(a); \
+    a.turns = TPR <= 32 && NV == 1 ? fwd_turns(a.rows, RPC) : 1;                                          \
+    const long long per = (long long)RPC * a.turns;                                                       \
+    kda_rms_norm_fwd_kernel<T, VEC, TPR, NV, QUANT><<<(unsigned)((a.rows + per - 1) / per), NT, 0, st>>>(a); \
     return cudaGetLastError();                                                                            \
   }
   KDA_NORM_SHAPES(KDA_CASE)
   if constexpr (VEC < 8) { KDA_NORM_SHAPES_LONG(KDA_CASE) }
   if constexpr (VEC == 1) { KDA_NORM_SHAPES_SCALAR(KDA_CASE) }
 #undef KDA_CASE
+  return cudaErrorInvalidValue;
+}
+// The group modes of a vector width.
+template <typename T, int VEC>
+cudaError_t launch_fwd_groups(const FwdArgs& a, cudaStream_t st) {
+  switch (a.group / VEC) {
+    case 4: return launch_fwd<T, VEC, 4>(a, st);
+    case 8: return launch_fwd<T, VEC, 8>(a, st);
+    case 16: return launch_fwd<T, VEC, 16>(a, st);
+    case 32: return launch_fwd<T, VEC, 32>(a, st);
+  }
   return cudaErrorInvalidValue;
 }
 
