@@ -162,6 +162,58 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 __device__ __forceinline__ float2 dup2(float a) { return make_float2(a, a); }
+// x *= y, pairwise where the length allows
+template <int N>
+__device__ __forceinline__ void scale_by(float (&x)[N], const float (&y)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float2 v = mul2(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]));
+      x[e] = v.x;
+      x[e + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] *= y[e];
+  }
+}
+template <int N>
+__device__ __forceinline__ void scale_by(float (&x)[N], float y) {
+  float d[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) d[e] = y;
+  scale_by<N>(x, d);
+}
+// acc += x y
+template <int N>
+__device__ __forceinline__ void add_scaled(float (&acc)[N], const float (&x)[N], float y) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float2 v = fma2(make_float2(x[e], x[e + 1]), dup2(y), make_float2(acc[e], acc[e + 1]));
+      acc[e] = v.x;
+      acc[e + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = fmaf(x[e], y, acc[e]);
+  }
+}
+// sum of x y, in two partial sums where the length allows
+template <int N>
+__device__ __forceinline__ float dot(const float (&x)[N], const float (&y)[N]) {
+  if constexpr (N % 2 == 0) {
+    float2 s = mul2(make_float2(x[0], x[1]), make_float2(y[0], y[1]));
+#pragma unroll
+    for (int e = 2; e < N; e += 2) s = fma2(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]), s);
+    return s.x + s.y;
+  } else {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) s = fmaf(x[e], y[e], s);
+    return s;
+  }
+}
 
 // Column sums of `lines` rows of src, `cols` wide, each in row order within 32
 // slices: columns below `split` go to dst0, the rest to dst1 (either may be

@@ -98,37 +98,70 @@ constexpr int threads_of(int tpr) { return tpr <= 32 ? 128 : tpr; }  // a row of
 // its own loads and exchanges.
 constexpr int rows_at_once(int tpr, int nv) { return tpr <= 32 && nv == 1 ? 2 : 1; }
 
+// Rows in turn (rows of one vector a thread, at most a warp): inputs arrive by
+// asynchronous copies kRing - 1 turns ahead, in a ring that each thread has to
+// itself (a turn ahead in registers: 84 us for 524288 rows of 128, 36% of the
+// copy rate).
+constexpr int kRing = 4;
+
 template <typename T, int VEC, int TPR, int NV, int QUANT>
-__global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 && NV == 1 ? 7 : 1)
-    kda_rms_norm_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const FwdArgs a) {
   constexpr int NT = threads_of(TPR);
   constexpr int RPC = NT / TPR;  // row slots of a CTA
   constexpr int RU = rows_at_once(TPR, NV);
-  constexpr bool kAhead = TPR <= 32 && NV == 1;  // several turns, the next one's rows loaded during one
+  constexpr bool kTurns = TPR <= 32 && NV == 1;
+  constexpr bool kAsync = kTurns && VEC > 1;
   constexpr int GL = QUANT >= kGroup ? QUANT : 1;  // lanes of one group
   __shared__ float s_red[2][RU][32];
+  __shared__ Pack<T, VEC> s_in[kAsync ? kRing : 1][kAsync ? RU : 1][2][kAsync ? NT : 1];
   const int j = threadIdx.x % TPR;
   const int nvec = a.D / VEC;
-  const T* xp = static_cast<const T*>(a.x) + j * VEC;
-  const T* rp = a.residual ? static_cast<const T*>(a.residual) + j * VEC : nullptr;
-  const int turns = kAhead ? a.turns : 1;
-  long long row0 = ((long long)blockIdx.x * turns * RPC + threadIdx.x / TPR) * RU;
+  const int turns = kTurns ? a.turns : 1;
+  long long row0 = ((long long)blockIdx.x * turns * RPC + threadIdx.x / TPR) * RU;  // the thread's first row
   const long long step = (long long)RPC * RU;
+  const T* xp = static_cast<const T*>(a.x) + row0 * a.x_stride + j * VEC;
+  const T* rp = a.residual ? static_cast<const T*>(a.residual) + row0 * a.D + j * VEC : nullptr;
 
   Pack<T, VEC> px[RU][NV], pr[RU][NV];
+  // rows past the end are not read and not written
   auto fetch = [&](long long first) {
+    if constexpr (!kAsync) {
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const long long row = first + u < a.rows ? first + u : a.rows - 1;
+      for (int u = 0; u < RU; ++u)
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (j + i * TPR < nvec) {
-          px[u][i] = load_pack<T, VEC>(xp + row * a.x_stride + i * TPR * VEC);
-          if (rp) pr[u][i] = load_pack<T, VEC>(rp + row * a.D + i * TPR * VEC);
-        }
+        for (int i = 0; i < NV; ++i)
+          if (first + u < a.rows && j + i * TPR < nvec) {
+            px[u][i] = load_pack<T, VEC>(xp + u * a.x_stride + i * TPR * VEC);
+            if (rp) pr[u][i] = load_pack<T, VEC>(rp + u * a.D + i * TPR * VEC);
+          }
+      xp += step * a.x_stride;
+      if (rp) rp += step * a.D;
     }
   };
-  fetch(row0);
+  int ahead = 0, slot = 0;  // turns staged; the ring's slot to fill
+  auto stage = [&] {
+    if constexpr (kAsync) {
+      if (ahead < turns && j < nvec) {
+#pragma unroll
+        for (int u = 0; u < RU; ++u)
+          if (row0 + ahead * step + u < a.rows) {
+            copy_async<sizeof(T) * VEC>(&s_in[slot][u][0][threadIdx.x], xp + u * a.x_stride);
+            if (rp) copy_async<sizeof(T) * VEC>(&s_in[slot][u][1][threadIdx.x], rp + u * a.D);
+          }
+      }
+      copy_async_commit();
+      xp += step * a.x_stride;
+      if (rp) rp += step * a.D;
+      ++ahead;
+      slot = slot + 1 < kRing ? slot + 1 : 0;
+    }
+  };
+  if constexpr (kAsync) {
+#pragma unroll
+    for (int g = 0; g < kRing - 1; ++g) stage();
+  } else {
+    fetch(row0);
+  }
   float w[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -138,20 +171,32 @@ __global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 && NV == 1 ? 7 : 1)
       for (int e = 0; e < VEC; ++e) w[i][e] = 0.f;
   }
   const float inv_d = 1.f / (float)a.D;
+  char* yp = static_cast<char*>(a.y) + (row0 * a.D + j * VEC) * (QUANT == kNone ? sizeof(T) : 1);
+  T* sp = a.s ? static_cast<T*>(a.s) + row0 * a.D + j * VEC : nullptr;
+  float* scp = QUANT != kNone ? a.scale + row0 * a.groups + (QUANT >= kGroup ? j / GL : 0) : nullptr;
+  const long long first_row = row0;
+  int read = 0;
 #pragma unroll 1
-  for (int turn = 0; turn < turns; ++turn, row0 += step) {
+  for (int turn = 0; turn < turns; ++turn) {
     if (RPC > 1 && row0 - threadIdx.x / TPR * RU >= a.rows) return;  // (uniform: a CTA's slots are consecutive rows)
     float v[RU][NV][VEC], acc[RU];
+    if constexpr (kAsync) {
+      const long long at = row0;
+      row0 = first_row;  // stage() counts from the first turn
+      stage();
+      row0 = at;
+      copy_async_wait<kRing - 1>();
+    }
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       acc[u] = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (j + i * TPR < nvec) {
-          unpack<T, VEC>(px[u][i], v[u][i]);
+        if (row0 + u < a.rows && j + i * TPR < nvec) {
+          unpack<T, VEC>(kAsync ? s_in[read][kAsync ? u : 0][0][kAsync ? threadIdx.x : 0] : px[u][i], v[u][i]);
           if (rp) {
             float q[VEC];
-            unpack<T, VEC>(pr[u][i], q);
+            unpack<T, VEC>(kAsync ? s_in[read][kAsync ? u : 0][1][kAsync ? threadIdx.x : 0] : pr[u][i], q);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[u][i][e] += q[e];
           }
@@ -159,22 +204,18 @@ __global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 && NV == 1 ? 7 : 1)
 #pragma unroll
           for (int e = 0; e < VEC; ++e) v[u][i][e] = 0.f;
         }
+        acc[u] += dot<VEC>(v[u][i], v[u][i]);
       }
     }
-    if (kAhead && turn + 1 < turns) fetch(row0 + step);
-#pragma unroll
-    for (int u = 0; u < RU; ++u)
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[u] = fmaf(v[u][i][e], v[u][i][e], acc[u]);
-    if (a.s) {
+    if (kAsync) read = read + 1 < kRing ? read + 1 : 0;
+    if (!kAsync && turn + 1 < turns) fetch(row0 + step);
+    if (sp) {
 #pragma unroll
       for (int u = 0; u < RU; ++u)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (row0 + u < a.rows && j + i * TPR < nvec)
-            store_pack<T, VEC>(static_cast<T*>(a.s) + (row0 + u) * a.D + (j + i * TPR) * VEC, v[u][i]);
+          if (row0 + u < a.rows && j + i * TPR < nvec) store_pack<T, VEC>(sp + u * a.D + i * TPR * VEC, v[u][i]);
+      sp += step * a.D;
     }
     // the sum is taken of the unrounded s (the stored s is rounded once, to T)
     row_reduce<TPR, false>(acc, s_red[0]);
@@ -184,12 +225,13 @@ __global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 && NV == 1 ? 7 : 1)
       const float r = rsqrtf(acc[u] * inv_d + a.eps);
       amax[u] = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        scale_by<VEC>(v[u][i], r);
+        scale_by<VEC>(v[u][i], w[i]);
+        if (QUANT == kRow)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          v[u][i][e] = v[u][i][e] * r * w[i][e];
-          if (QUANT == kRow) amax[u] = max_nan(amax[u], fabsf(v[u][i][e]));
-        }
+          for (int e = 0; e < VEC; ++e) amax[u] = max_nan(amax[u], fabsf(v[u][i][e]));
+      }
     }
     if constexpr (QUANT == kNone) {
 #pragma unroll
@@ -197,7 +239,8 @@ __global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 && NV == 1 ? 7 : 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (row0 + u < a.rows && j + i * TPR < nvec)
-            store_pack<T, VEC>(static_cast<T*>(a.y) + (row0 + u) * a.D + (j + i * TPR) * VEC, v[u][i]);
+            store_pack<T, VEC>(reinterpret_cast<T*>(yp) + u * a.D + i * TPR * VEC, v[u][i]);
+      yp += step * a.D * sizeof(T);
     } else {
       if constexpr (QUANT == kRow) row_reduce<TPR, true>(amax, s_red[1]);
 #pragma unroll
@@ -214,20 +257,24 @@ __global__ void __launch_bounds__(threads_of(TPR), TPR <= 32 && NV == 1 ? 7 : 1)
 #pragma unroll
             for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
           }
+          // m / 448, within a unit in the last place; the floor's quotient is exact
+          const bool floored = m <= kScaleFloor;
           m = max_nan(m, kScaleFloor);
-          if (live && c < nvec && (QUANT >= kGroup ? c % GL == 0 : c == 0))
-            a.scale[(row0 + u) * a.groups + (QUANT >= kGroup ? c / GL : 0)] = m / kFp8Max;
+          if (live && c < nvec && (QUANT >= kGroup ? j % GL == 0 : c == 0))
+            scp[u * a.groups + (QUANT >= kGroup ? i * (TPR / GL) : 0)] =
+                floored ? kScaleFloor / kFp8Max : m * (1.f / kFp8Max);
           // 448 / m: the reciprocal's argument scaled down, so that a huge m does not flush it to 0
           const float inv = fast_rcp(m * 0x1p-10f) * (kFp8Max * 0x1p-10f);
           if (live && c < nvec) {
-            float q[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) q[e] = v[u][i][e] * inv;
-            store_fp8<VEC>(static_cast<uint8_t*>(a.y) + (row0 + u) * a.D + c * VEC, q);
+            scale_by<VEC>(v[u][i], inv);
+            store_fp8<VEC>(reinterpret_cast<uint8_t*>(yp) + u * a.D + i * TPR * VEC, v[u][i]);
           }
         }
       }
+      yp += step * a.D;
+      scp += step * a.groups;
     }
+    row0 += step;
   }
 }
 
@@ -249,12 +296,21 @@ struct BwdArgs {
   float eps;
 };
 
+// Rows of up to two vectors a thread arrive by asynchronous copies, two turns
+// ahead, in a ring that each thread has to itself.
+constexpr int kBwdRing = 3;
+constexpr bool bwd_async(int vec, int nv) { return vec > 1 && nv <= 2; }
+
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / threads_of(TPR) : 1) kda_rms_norm_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(threads_of(TPR), bwd_async(VEC, NV) ? 512 / threads_of(TPR) : 1)
+    kda_rms_norm_bwd_kernel(const BwdArgs a) {
   constexpr int NT = threads_of(TPR);
   constexpr int RPC = NT / TPR;
   constexpr bool kKeepW = NV * VEC <= 16;  // weights in registers, or read again for each row
-  constexpr bool kAhead = NV * VEC <= 16;   // the next row's loads in registers, or longer rows hide their own
+  constexpr bool kAsync = bwd_async(VEC, NV);
+  constexpr bool kAhead = !kAsync && NV * VEC <= 16;  // the next row's loads in registers; longer rows hide their own
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  auto ring = reinterpret_cast<Pack<T, VEC>(*)[3][NV][NT]>(smem_raw);  // dy, s, ds
   __shared__ float s_red[2][2][32];
   const int j = threadIdx.x % TPR;
   const int nvec = a.D / VEC;
@@ -278,7 +334,29 @@ __global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / thread
       }
     }
   };
-  if (kAhead) fetch((long long)blockIdx.x * RPC + threadIdx.x / TPR);
+  int slot = 0, read = 0;
+  auto stage = [&](long long row) {
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = j + i * TPR;
+        if (row < a.rows && c < nvec) {
+          const long long at = row * a.D + (long long)c * VEC;
+          copy_async<sizeof(T) * VEC>(&ring[slot][0][i][threadIdx.x], static_cast<const T*>(a.dy) + at);
+          copy_async<sizeof(T) * VEC>(&ring[slot][1][i][threadIdx.x], static_cast<const T*>(a.s) + at);
+          if (a.ds) copy_async<sizeof(T) * VEC>(&ring[slot][2][i][threadIdx.x], static_cast<const T*>(a.ds) + at);
+        }
+      }
+      copy_async_commit();
+      slot = slot + 1 < kBwdRing ? slot + 1 : 0;
+    }
+  };
+  const long long own = (long long)blockIdx.x * RPC + threadIdx.x / TPR;
+  if constexpr (kAsync) {
+#pragma unroll
+    for (int g = 0; g < kBwdRing - 1; ++g) stage(own + g * step);
+  }
+  if (kAhead) fetch(own);
   int buf = 0;
   const float inv_d = 1.f / (float)a.D;
   // every row slot of the CTA runs the same number of turns (reductions are CTA-wide or warp-wide)
@@ -287,14 +365,19 @@ __global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / thread
     const bool live = row < a.rows;
     float g[NV][VEC], v[NV][VEC];
     Pack<T, VEC> d[kAhead ? NV : 1];
-    if (!kAhead) fetch(row);
+    if constexpr (kAsync) {
+      stage(row + (kBwdRing - 1) * step);
+      copy_async_wait<kBwdRing - 1>();
+    } else if (!kAhead) {
+      fetch(row);
+    }
     float sums[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = j + i * TPR;
       if (live && c < nvec) {
-        unpack<T, VEC>(pg[i], g[i]);
-        unpack<T, VEC>(ps[i], v[i]);
+        unpack<T, VEC>(kAsync ? ring[read][0][i][threadIdx.x] : pg[i], g[i]);
+        unpack<T, VEC>(kAsync ? ring[read][1][i][threadIdx.x] : ps[i], v[i]);
         if (kAhead && a.ds) d[kAhead ? i : 0] = pd[i];
       } else {
 #pragma unroll
@@ -305,14 +388,13 @@ __global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / thread
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (j + i * TPR < nvec) {
-        float wv[VEC];
-        if (!kKeepW) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, wv);
+        float gw[VEC];
+        if (!kKeepW) load_param<VEC>(a.weight, a.w_bf16, (long long)(j + i * TPR) * VEC, gw);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float we = kKeepW ? w[kKeepW ? i : 0][e] : wv[e];
-          sums[0] = fmaf(v[i][e], v[i][e], sums[0]);
-          sums[1] = fmaf(g[i][e] * we, v[i][e], sums[1]);
-        }
+        for (int e = 0; e < VEC; ++e) gw[e] = kKeepW ? w[kKeepW ? i : 0][e] : gw[e];
+        scale_by<VEC>(gw, g[i]);
+        sums[0] += dot<VEC>(v[i], v[i]);
+        sums[1] += dot<VEC>(gw, v[i]);
       }
     }
     row_reduce<TPR, false>(sums, s_red[buf]);
@@ -323,22 +405,28 @@ __global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / thread
       for (int i = 0; i < NV; ++i) {
         const int c = j + i * TPR;
         if (c < nvec) {
-          float wv[VEC], o[VEC];
+          float o[VEC] = {}, wv[VEC], gv[VEC];
+          if (a.ds) {
+            if constexpr (kAsync) unpack<T, VEC>(ring[read][2][i][threadIdx.x], o);
+            else if constexpr (kAhead) unpack<T, VEC>(d[kAhead ? i : 0], o);
+            else load_f32<T, VEC>(static_cast<const T*>(a.ds) + row * a.D + (long long)c * VEC, o);
+          }
           if (!kKeepW) load_param<VEC>(a.weight, a.w_bf16, (long long)c * VEC, wv);
-          float de[VEC] = {};
-          if (a.ds)
-            unpack<T, VEC>(kAhead ? d[kAhead ? i : 0]
-                                  : load_pack<T, VEC>(static_cast<const T*>(a.ds) + row * a.D + (long long)c * VEC), de);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float we = kKeepW ? w[kKeepW ? i : 0][e] : wv[e];
-            dw[i][e] = fmaf(g[i][e] * v[i][e], r, dw[i][e]);
-            o[e] = fmaf(r * we, g[i][e], fmaf(-k, v[i][e], de[e]));
+            wv[e] = kKeepW ? w[kKeepW ? i : 0][e] : wv[e];
+            gv[e] = g[i][e];
           }
+          scale_by<VEC>(gv, v[i]);
+          add_scaled<VEC>(dw[i], gv, r);
+          add_scaled<VEC>(o, v[i], -k);
+          scale_by<VEC>(wv, g[i]);
+          add_scaled<VEC>(o, wv, r);
           store_pack<T, VEC>(static_cast<T*>(a.dx) + row * a.D + (long long)c * VEC, o);
         }
       }
     }
+    if (kAsync) read = read + 1 < kBwdRing ? read + 1 : 0;
   }
   if constexpr (RPC > 1) {  // the row slots of the CTA, added in order
     __shared__ __align__(16) float s_dw[RPC][TPR * VEC * NV];
@@ -443,8 +531,18 @@ cudaError_t launch_bwd(const BwdArgs& a, float* dweight, cudaStream_t st) {
   cudaError_t e = cudaErrorInvalidValue;
 #define KDA_CASE(TPR, NV)                                                                          \
   if (sh.tpr == TPR && sh.nv == NV) {                                                               \
-    kda_rms_norm_bwd_kernel<T, VEC, TPR, NV><<<grid, threads_of(TPR), 0, st>>>(a);              \
-    e = cudaGetLastError();                                                                          \
+    constexpr size_t bytes =                                                                         \
+        bwd_async(VEC, NV) ? (size_t)kBwdRing * 3 * NV * threads_of(TPR) * VEC * sizeof(T) : 0;         \
+    if (bytes > 48 * 1024) {                                                                          \
+      static PerDeviceOnce once;                                                                      \
+      e = run_once_per_device(once, [] {                                                              \
+        return cudaFuncSetAttribute(kda_rms_norm_bwd_kernel<T, VEC, TPR, NV>,                         \
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);         \
+      });                                                                                             \
+      if (e != cudaSuccess) return e;                                                                 \
+    }                                                                                                 \
+    kda_rms_norm_bwd_kernel<T, VEC, TPR, NV><<<grid, threads_of(TPR), bytes, st>>>(a);                \
+    e = cudaGetLastError();                                                                           \
   }
   KDA_NORM_SHAPES_BWD(KDA_CASE)
   if constexpr (VEC < 8) { KDA_NORM_SHAPES_LONG(KDA_CASE) }
