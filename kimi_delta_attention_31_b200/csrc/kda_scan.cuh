@@ -49,7 +49,8 @@ struct Args {
   const void* dy;    // [tokens, d]
   const float* dS;   // [N, d, S] or nullptr
   float* exitg;      // [chunks, d, S]: as entry, for the gradient that comes from the right
-  bool wide;         // the inputs can be copied 16 bytes at a time
+  int copy, copy_bc;  // bytes of one asynchronous copy of x, dt, z, dy and of B, C: 16, 8, 4, or 0 for 16-bit
+                      // elements at odd places, which are loaded and stored one by one
 };
 
 template <int S>
@@ -120,20 +121,23 @@ __device__ __forceinline__ float2 decay2(float2 delta, float2 A2) {
   return make_float2(ex2(e.x), ex2(e.y));
 }
 
-template <int N>
+// A lane's states: 2 N of them, four adjacent ones at a time, the next four
+// STRIDE further (the lanes of a channel take turns, so that what they read
+// together is adjacent).
+template <int N, int STRIDE>
 __device__ __forceinline__ void load_state(const float* p, float2 (&h)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float4 v = *reinterpret_cast<const float4*>(p + 2 * i);
+    const float4 v = *reinterpret_cast<const float4*>(p + i / 2 * STRIDE);
     h[i] = make_float2(v.x, v.y);
     h[i + 1] = make_float2(v.z, v.w);
   }
 }
-template <int N>
+template <int N, int STRIDE>
 __device__ __forceinline__ void store_state(float* p, const float2 (&h)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 2)
-    *reinterpret_cast<float4*>(p + 2 * i) = make_float4(h[i].x, h[i].y, h[i + 1].x, h[i + 1].y);
+    *reinterpret_cast<float4*>(p + i / 2 * STRIDE) = make_float4(h[i].x, h[i].y, h[i + 1].x, h[i + 1].y);
 }
 template <int N>
 __device__ __forceinline__ void zero_state(float2 (&h)[N]) {
@@ -151,33 +155,45 @@ struct alignas(16) TileSmem {
   static constexpr int NIN = MODE == 0 ? 3 : MODE == 1 ? 2 : 4;  // x, dt (, z (, dy))
   T in[kStages][NIN][kTile][CH];
   T raw[kStages][MODE == 1 ? 1 : 2][kTile][S];  // B, C as they are in memory
-  float B[2][kTile][S];
-  float C[MODE == 1 ? 1 : 2][MODE == 1 ? 1 : kTile][MODE == 1 ? 4 : S];
+  static constexpr bool kConvert = sizeof(T) != 4;  // fp32 ones are read where they are
+  float B[2][kConvert ? kTile : 1][kConvert ? S : 4];
+  float C[2][kConvert && MODE != 1 ? kTile : 1][kConvert && MODE != 1 ? S : 4];
   float4 du[kStep][CH];                         // delta twice, delta x twice
   float gv[MODE == 2 ? kStep : 1][CH];          // dy silu(z)
 };
 
-// `rows` rows of `len` elements (len <= WIDTH), `stride` apart, to dst[.][WIDTH]:
-// 16 bytes a copy, or one element each (32-bit ones asynchronously too).
-template <typename T, int WIDTH>
+// `rows` rows of `len` elements (len <= WIDTH), `stride` apart, to dst[.][WIDTH],
+// ROWS of them at most, by THREADS threads: `bytes` a copy.  The narrow copies
+// stay out of line: they would push the scan's own loop out of the instruction
+// cache (4% on 16-byte inputs).
+template <typename T, int WIDTH, int THREADS>
+__device__ __noinline__ void stage_rows_narrow(T (*dst)[WIDTH], const T* src, long long stride, int rows, int len,
+                                               int bytes) {
+  const int shift = bytes == 8 ? (sizeof(T) == 2 ? 2 : 1) : bytes == 4 && sizeof(T) == 2 ? 1 : 0;  // elements: 1 << shift
+  const int n = WIDTH >> shift;  // copies a row
+#pragma unroll 4
+  for (int e = threadIdx.x; e < rows * n; e += THREADS) {
+    const int r = e / n, k = (e - r * n) << shift;
+    if (k >= len) continue;
+    const T* p = src + r * stride + k;
+    const int have = (len - k) * (int)sizeof(T);
+    if (bytes == 8) copy_async<8>(&dst[r][k], p, min(8, have));
+    else if (bytes == 4) copy_async<4>(&dst[r][k], p, min(4, have));
+    else dst[r][k] = *p;
+  }
+}
+template <typename T, int WIDTH, int ROWS, int THREADS>
 __device__ __forceinline__ void stage_rows(T (*dst)[WIDTH], const T* src, long long stride, int rows, int len,
-                                           bool wide) {
-  if (wide) {
+                                           int bytes) {
+  if (bytes == 16) {
     constexpr int PER = 16 / sizeof(T), N = WIDTH / PER;  // copies a row
 #pragma unroll
-    for (int i = 0; i < (kTile * N + kThreads - 1) / kThreads; ++i) {
-      const int e = i * kThreads + (int)threadIdx.x, r = e / N, k = (e % N) * PER;
+    for (int i = 0; i < (ROWS * N + THREADS - 1) / THREADS; ++i) {
+      const int e = i * THREADS + (int)threadIdx.x, r = e / N, k = (e % N) * PER;
       if (r < rows && k < len) copy_async<16>(&dst[r][k], src + r * stride + k, min(16, (len - k) * (int)sizeof(T)));
     }
   } else {
-#pragma unroll 1
-    for (int e = threadIdx.x; e < rows * WIDTH; e += kThreads) {
-      const int r = e / WIDTH, k = e % WIDTH;
-      if (k < len) {
-        if constexpr (sizeof(T) == 4) copy_async<4>(&dst[r][k], src + r * stride + k);
-        else dst[r][k] = src[r * stride + k];
-      }
-    }
+    stage_rows_narrow<T, WIDTH, THREADS>(dst, src, stride, rows, len, bytes);
   }
 }
 
@@ -210,16 +226,16 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   const int width = a.cpg - cl0 < CH ? a.cpg - cl0 : CH;  // channels of the CTA
   const bool active = ch < width;  // the others compute on whatever shared memory holds and write nothing
   const long long c0 = (long long)grp * a.cpg + cl0, c = c0 + (active ? ch : width - 1);
-  const long long crow = c * S + sl * SPT;
+  const long long crow = c * S + sl * 4;
 
   if (blockIdx.x == 0) check_seq_table(a.q);
   if (MODE == kForward && chunk == 0 && a.S_out) {  // sequences without tokens keep their state
     for (int n = 0; n < a.q.num; ++n)
       if (seq_empty(a.q, n) && active) {
         float2 v[NP];
-        if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, v);
+        if (a.S0) load_state<NP, LPC * 4>(a.S0 + (long long)n * a.d * S + crow, v);
         else zero_state<NP>(v);
-        store_state<NP>(a.S_out + (long long)n * a.d * S + crow, v);
+        store_state<NP, LPC * 4>(a.S_out + (long long)n * a.d * S + crow, v);
       }
   }
   const long long t0 = chunk * a.L;
@@ -230,31 +246,33 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   auto stage = [&](long long t, int st) {
     if (t < t1) {
       const int rows = t1 - t < kTile ? (int)(t1 - t) : kTile;
-      stage_rows<T, CH>(sm.in[st][0], static_cast<const T*>(a.x) + t * a.xs + c0, a.xs, rows, width, a.wide);
-      stage_rows<T, CH>(sm.in[st][1], static_cast<const T*>(a.dt) + t * a.dts + c0, a.dts, rows, width, a.wide);
+      stage_rows<T, CH, kTile, kThreads>(sm.in[st][0], static_cast<const T*>(a.x) + t * a.xs + c0, a.xs, rows, width, a.copy);
+      stage_rows<T, CH, kTile, kThreads>(sm.in[st][1], static_cast<const T*>(a.dt) + t * a.dts + c0, a.dts, rows, width, a.copy);
       if constexpr (kZ)
         if (gated)
-          stage_rows<T, CH>(sm.in[st][kZ ? 2 : 0], static_cast<const T*>(a.z) + t * a.zs + c0, a.zs, rows, width,
-                            a.wide);
+          stage_rows<T, CH, kTile, kThreads>(sm.in[st][kZ ? 2 : 0], static_cast<const T*>(a.z) + t * a.zs + c0, a.zs, rows, width,
+                            a.copy);
       if constexpr (MODE == kLocalBwd)
-        stage_rows<T, CH>(sm.in[st][MODE == kLocalBwd ? 3 : 0], static_cast<const T*>(a.dy) + t * a.d + c0, a.d, rows,
-                          width, a.wide);
-      stage_rows<T, S>(sm.raw[st][0], static_cast<const T*>(a.B) + t * a.bs + (long long)grp * S, a.bs, rows, S,
-                       a.wide);
+        stage_rows<T, CH, kTile, kThreads>(sm.in[st][MODE == kLocalBwd ? 3 : 0], static_cast<const T*>(a.dy) + t * a.d + c0, a.d, rows,
+                          width, a.copy);
+      stage_rows<T, S, kTile, kThreads>(sm.raw[st][0], static_cast<const T*>(a.B) + t * a.bs + (long long)grp * S, a.bs, rows, S,
+                       a.copy_bc);
       if constexpr (kC)
-        stage_rows<T, S>(sm.raw[st][kC ? 1 : 0], static_cast<const T*>(a.C) + t * a.cs + (long long)grp * S, a.cs, rows,
-                         S, a.wide);
+        stage_rows<T, S, kTile, kThreads>(sm.raw[st][kC ? 1 : 0], static_cast<const T*>(a.C) + t * a.cs + (long long)grp * S, a.cs, rows,
+                         S, a.copy_bc);
     }
     copy_async_commit();
   };
   // B, C of a tile in fp32 (a barrier before and after); rows past the chunk are not used
   auto convert = [&](int st, int buf) {
+    if constexpr (TileSmem<T, S, MODE>::kConvert) {
 #pragma unroll
-    for (int i = 0; i < (kTile * S + kThreads - 1) / kThreads; ++i) {
-      const int e = i * kThreads + (int)threadIdx.x;
-      if (e < kTile * S) {
-        (&sm.B[buf][0][0])[e] = to_f32<T>((&sm.raw[st][0][0][0])[e]);
-        if constexpr (kC) (&sm.C[kC ? buf : 0][0][0])[e] = to_f32<T>((&sm.raw[st][kC ? 1 : 0][0][0])[e]);
+      for (int i = 0; i < (kTile * S + kThreads - 1) / kThreads; ++i) {
+        const int e = i * kThreads + (int)threadIdx.x;
+        if (e < kTile * S) {
+          (&sm.B[buf][0][0])[e] = to_f32<T>((&sm.raw[st][0][0][0])[e]);
+          if constexpr (kC) (&sm.C[buf][0][0])[e] = to_f32<T>((&sm.raw[st][kC ? 1 : 0][0][0])[e]);
+        }
       }
     }
   };
@@ -262,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   stage(t0 + kTile, 1);
 
   float2 A2[NP], h[NP];
-  load_state<NP>(a.A + crow, A2);
+  load_state<NP, LPC * 4>(a.A + crow, A2);
 #pragma unroll
   for (int i = 0; i < NP; ++i) A2[i] = mul2(A2[i], dup2(kLog2eF));
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
@@ -271,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   int n = seq_of_token(a.q, t0);
   long long end = seq_end(a.q, n);
   bool cut = seq_start(a.q, n) == t0;
-  if (cut && a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
-  else if (!cut && MODE == kForward && a.entry) load_state<NP>(a.entry + chunk * a.d * S + crow, h);
+  if (cut && a.S0) load_state<NP, LPC * 4>(a.S0 + (long long)n * a.d * S + crow, h);
+  else if (!cut && MODE == kForward && a.entry) load_state<NP, LPC * 4>(a.entry + chunk * a.d * S + crow, h);
   else zero_state<NP>(h);
   constexpr int NPB = MODE == kLocalBwd ? NP : 1;
   float2 P[NPB], R[NPB];  // kLocalBwd: product of the decays so far, gradient sent to the left
@@ -294,11 +312,11 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   T* yp = MODE == kForward ? static_cast<T*>(a.y) + (t0 + own0) * a.d + c : nullptr;
 
   auto next_sequence = [&](long long t) {
-    if (MODE == kForward && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
+    if (MODE == kForward && a.S_out && active) store_state<NP, LPC * 4>(a.S_out + (long long)n * a.d * S + crow, h);
     n = seq_of_token(a.q, t);
     end = seq_end(a.q, n);
     cut = true;
-    if (a.S0) load_state<NP>(a.S0 + (long long)n * a.d * S + crow, h);
+    if (a.S0) load_state<NP, LPC * 4>(a.S0 + (long long)n * a.d * S + crow, h);
     else zero_state<NP>(h);
     if (MODE == kLocalBwd) zero_state<NPB>(P);
   };
@@ -307,12 +325,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
     float2 acc = dup2(0.f);
 #pragma unroll
     for (int p = 0; p < NP; p += 2) {
-      const float4 b4 = *reinterpret_cast<const float4*>(tb + sl * SPT + 2 * p);
+      const float4 b4 = *reinterpret_cast<const float4*>(tb + (p / 2 * LPC + sl) * 4);
       const float2 w0 = decay2(dd, A2[p]), w1 = decay2(dd, A2[p + 1]);
       h[p] = fma2(w0, h[p], mul2(uu, make_float2(b4.x, b4.y)));
       h[p + 1] = fma2(w1, h[p + 1], mul2(uu, make_float2(b4.z, b4.w)));
       if constexpr (kC) {
-        const float4 c4 = *reinterpret_cast<const float4*>(tc + sl * SPT + 2 * p);
+        const float4 c4 = *reinterpret_cast<const float4*>(tc + (p / 2 * LPC + sl) * 4);
         if constexpr (MODE == kForward) {
           acc = p == 0 ? mul2(h[p], make_float2(c4.x, c4.y)) : fma2(h[p], make_float2(c4.x, c4.y), acc);
           acc = fma2(h[p + 1], make_float2(c4.z, c4.w), acc);
@@ -321,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
           P[p + 1] = mul2(P[p + 1], w1);
           float2 g0 = mul2(dup2(gv), make_float2(c4.x, c4.y)), g1 = mul2(dup2(gv), make_float2(c4.z, c4.w));
           if (last) {
-            const float4 s4 = *reinterpret_cast<const float4*>(a.dS + (long long)n * a.d * S + crow + 2 * p);
+            const float4 s4 = *reinterpret_cast<const float4*>(a.dS + (long long)n * a.d * S + crow + p / 2 * LPC * 4);
             g0 = add2(g0, make_float2(s4.x, s4.y));
             g1 = add2(g1, make_float2(s4.z, s4.w));
           }
@@ -344,6 +362,14 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
     stage(t + 2 * kTile, st2);
     if (t + kTile < t1) convert(st1, buf ^ 1);
     const T(*in)[kTile][CH] = sm.in[st];
+    const float *Bt, *Ct;  // this tile's B, C, S numbers a token
+    if constexpr (TileSmem<T, S, MODE>::kConvert) {
+      Bt = &sm.B[buf][0][0];
+      Ct = &sm.C[buf][0][0];
+    } else {
+      Bt = &sm.raw[st][0][0][0];
+      Ct = &sm.raw[st][kC ? 1 : 0][0][0];
+    }
 #pragma unroll 1
     for (int s0 = 0; s0 < kTile && t + s0 < t1; s0 += kStep) {
       const long long ts = t + s0;
@@ -379,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
           const float4 du = sm.du[i][ch];
-          yv[i] = token(make_float2(du.x, du.y), make_float2(du.z, du.w), MODE == kLocalBwd ? sm.gv[MODE == kLocalBwd ? i : 0][ch] : 0.f, sm.B[buf][s0 + i],
-                        kC ? sm.C[kC ? buf : 0][kC ? s0 + i : 0] : nullptr, false);
+          yv[i] = token(make_float2(du.x, du.y), make_float2(du.z, du.w), MODE == kLocalBwd ? sm.gv[MODE == kLocalBwd ? i : 0][ch] : 0.f, Bt + (s0 + i) * S,
+                        Ct + (s0 + i) * S, false);
         }
         if constexpr (MODE == kForward) {
           int at;
@@ -404,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
             gv = zz * fast_sigmoid(zz);
           }
           if (MODE == kLocalBwd) gv *= to_f32<T>(in[MODE == kLocalBwd ? 3 : 0][s0 + i][ch]);
-          float y = token(dup2(delta), dup2(delta * xv), gv, sm.B[buf][s0 + i], kC ? sm.C[kC ? buf : 0][kC ? s0 + i : 0] : nullptr,
+          float y = token(dup2(delta), dup2(delta * xv), gv, Bt + (s0 + i) * S, Ct + (s0 + i) * S,
                           MODE == kLocalBwd && a.dS && ts + i + 1 == end);
           if (sl == 0) sumd += delta;
           if (MODE == kForward) {
@@ -420,13 +446,13 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
     st = st1;
   }
   if constexpr (MODE == kForward) {
-    if (t1 == end && a.S_out && active) store_state<NP>(a.S_out + (long long)n * a.d * S + crow, h);
+    if (t1 == end && a.S_out && active) store_state<NP, LPC * 4>(a.S_out + (long long)n * a.d * S + crow, h);
   } else {
 #pragma unroll
     for (int o = LPC / 2; o > 0; o >>= 1) sumd += __shfl_xor_sync(0xffffffffu, sumd, o);
     if (active) {
-      store_state<NP>(a.entry + chunk * a.d * S + crow, h);
-      if constexpr (MODE == kLocalBwd) store_state<NP>(a.exitg + chunk * a.d * S + crow, R);
+      store_state<NP, LPC * 4>(a.entry + chunk * a.d * S + crow, h);
+      if constexpr (MODE == kLocalBwd) store_state<NP, LPC * 4>(a.exitg + chunk * a.d * S + crow, R);
       if (sl == 0) a.sumd[chunk * a.d + c] = cut ? -1.f : sumd;
     }
   }
@@ -570,15 +596,18 @@ struct FwdPlan {
   bool split;
   long long L, chunks;
 };
-// Whether the inputs' addresses and strides allow copies of 16 bytes.  A CTA's
-// channels start at a multiple of 16 of their group.
-inline bool wide_copies(const Args& a, int esize) {
-  const long long per = 16 / esize;
+// The widest copy that every row of these inputs allows (null ones do not
+// count).  A CTA's channels start at a multiple of 16 of their group.
+inline int copy_width(std::initializer_list<const void*> ps, std::initializer_list<long long> strides, int esize) {
   uintptr_t low = 0;
-  for (const void* p : {a.x, a.dt, a.z, a.B, a.C, a.dy}) low |= reinterpret_cast<uintptr_t>(p);
-  bool ok = low % 16 == 0 && (a.cpg == a.d || a.cpg % per == 0) && (!a.dy || a.d % per == 0);
-  for (const long long s : {a.xs, a.dts, a.z ? a.zs : 0LL, a.bs, a.cs}) ok = ok && s % per == 0;
-  return ok;
+  for (const void* p : ps) low |= reinterpret_cast<uintptr_t>(p);
+  for (const long long s : strides) low |= (uintptr_t)(s * esize);
+  return low % 16 == 0 ? 16 : low % 8 == 0 ? 8 : low % 4 == 0 ? 4 : 0;
+}
+inline void set_copies(Args& a, int S, int esize) {
+  a.copy = copy_width({a.x, a.dt, a.z, a.dy},
+                      {a.xs, a.dts, a.z ? a.zs : 0, a.dy ? a.d : 0, a.cpg == a.d ? 0 : a.cpg}, esize);
+  a.copy_bc = copy_width({a.B, a.C}, {a.bs, a.cs, S}, esize);
 }
 inline FwdPlan fwd_plan(long long B, long long T, int num_seqs, int d, int groups, int S) {
   const long long tokens = B * T;
@@ -599,7 +628,7 @@ template <typename T, int S, int MODE>
 cudaError_t launch_scan(Args a, cudaStream_t st) {
   const long long grid = a.chunks * a.ncb;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  a.wide = wide_copies(a, (int)sizeof(T));
+  set_copies(a, S, (int)sizeof(T));
   constexpr size_t bytes = sizeof(TileSmem<T, S, MODE>);
   if (bytes > 48 * 1024) {
     static PerDeviceOnce once;

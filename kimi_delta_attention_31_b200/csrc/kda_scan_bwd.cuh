@@ -136,21 +136,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
 
   // the inputs of a slab, by asynchronous copies where their places allow it
   auto stage_one = [&](T(*dst)[kSlab], const void* src, long long stride, int slab0, int width) {
-    const T* p = static_cast<const T*>(src) + t0 * stride + gch + slab0;
-    if (a.wide) {
-      constexpr int PER = 16 / sizeof(T), N = kSlab / PER;
-#pragma unroll
-      for (int i = 0; i < (kTokens * N + kBwdThreads - 1) / kBwdThreads; ++i) {
-        const int e = i * kBwdThreads + tid, r = e / N, k = (e % N) * PER;
-        if (r < live && k < width) copy_async<16>(&dst[r][k], p + r * stride + k, min(16, (width - k) * (int)sizeof(T)));
-      }
-    } else {
-      for (int r = warp; r < live; r += kWarps)
-        if (lane < width) {
-          if constexpr (sizeof(T) == 4) copy_async<4>(&dst[r][lane], p + r * stride + lane);
-          else dst[r][lane] = p[r * stride + lane];
-        }
-    }
+    stage_rows<T, kSlab, kTokens, kBwdThreads>(dst, static_cast<const T*>(src) + t0 * stride + gch + slab0, stride, live,
+                                               width, a.copy);
   };
   auto stage_slab = [&](int slab) {
     const int slab0 = (cbl * o.slabs + slab) * kSlab;
@@ -513,7 +500,7 @@ cudaError_t launch_bwd(Args a, BwdOut o, float* dA, float* dB, float* dC, float*
     a.blocks_per_group = a.ncb / groups;
     if ((e = launch_scan<T, S, kLocalBwd>(a, st)) != cudaSuccess) return e;
     if ((e = launch_carry(a, S, true, st)) != cudaSuccess) return e;
-    a.wide = wide_copies(a, (int)sizeof(T));
+    set_copies(a, S, (int)sizeof(T));
     a.ncb = p.blocks_per_group * groups;
     a.blocks_per_group = p.blocks_per_group;
     static PerDeviceOnce once;
