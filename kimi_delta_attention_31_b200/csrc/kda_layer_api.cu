@@ -139,7 +139,7 @@ size_t norm_lines(long long rows, int D) {
   size_t most = 0;
   for (int vec : {8, 4, 1}) {
     if (D % vec || D / vec > kda::norm::kMaxDim / vec) continue;
-    const size_t lines = (size_t)kda::norm::bwd_grid(rows, D / vec);
+    const size_t lines = (size_t)kda::norm::bwd_grid(rows, D / vec, vec);
     if (lines > most) most = lines;
   }
   return most;

@@ -302,13 +302,13 @@ constexpr int kBwdRing = 3;
 constexpr bool bwd_async(int vec, int nv) { return vec > 1 && nv <= 2; }
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(threads_of(TPR), bwd_async(VEC, NV) ? 512 / threads_of(TPR) : 1)
+__global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / threads_of(TPR) : 1)
     kda_rms_norm_bwd_kernel(const BwdArgs a) {
   constexpr int NT = threads_of(TPR);
   constexpr int RPC = NT / TPR;
   constexpr bool kKeepW = NV * VEC <= 16;  // weights in registers, or read again for each row
   constexpr bool kAsync = bwd_async(VEC, NV);
-  constexpr bool kAhead = !kAsync && NV * VEC <= 16;  // the next row's loads in registers; longer rows hide their own
+  constexpr bool kAhead = VEC == 1 && NV <= 4;  // the next row's loads in registers; longer rows hide their own
   extern __shared__ __align__(16) unsigned char smem_raw[];
   auto ring = reinterpret_cast<Pack<T, VEC>(*)[3][NV][NT]>(smem_raw);  // dy, s, ds
   __shared__ float s_red[2][2][32];
@@ -449,34 +449,65 @@ __global__ void __launch_bounds__(threads_of(TPR), bwd_async(VEC, NV) ? 512 / th
   }
 }
 
-// Host: the row shapes built, smallest first.  `vecs` vectors a row: a vector a
-// thread as long as that gives a CTA of at most 512 threads.
+// Host: the row shapes built, smallest first.  `vecs` vectors a row of `vec`
+// elements.  Up to a warp a thread takes one vector.  Longer rows give each
+// thread two, which halves the exchanges between warps (rows of 2048 in bf16,
+// one vector against two: 31.6 and 27.5 us for 8192 e4m3 rows; four: no better);
+// rows read element by element take one warp group and up to 16 elements a
+// thread (60000 rows of 500: 61 us, with 512 threads and one element 147 us).
 struct RowShape {
   int tpr, nv;
 };
-inline RowShape row_shape(int vecs) {
-  for (int tpr = 8; tpr <= 512; tpr *= 2)
+inline RowShape row_shape(int vecs, int vec) {
+  for (int tpr = 8; tpr <= 32; tpr *= 2)
     if (vecs <= tpr) return {tpr, 1};
-  for (int nv : {2, 3, 4, 8, 16})
+  if (vec == 1) {
+    for (int nv : {1, 2, 5, 10, 16})
+      if (vecs <= 128 * nv) return {128, nv};
+    for (int nv : {8, 16})
+      if (vecs <= 512 * nv) return {512, nv};
+    return {512, 32};
+  }
+  for (int tpr = 64; tpr <= 128; tpr *= 2)
+    if (vecs <= tpr) return {tpr, 1};
+  for (int tpr = 128; tpr <= 512; tpr *= 2)
+    if (vecs <= 2 * tpr) return {tpr, 2};
+  for (int nv : {3, 4})
     if (vecs <= 512 * nv) return {512, nv};
-  return {512, 32};
+  return {512, 8};
+}
+// Backward: two vectors a thread where a row takes several warps, which keeps
+// enough loads in flight; element by element up to four a thread, then 512
+// threads (16000 rows of 1001: 85 us, with 128 threads of eight 145 us).
+inline RowShape row_shape_bwd(int vecs, int vec) {
+  for (int tpr = 8; tpr <= 32; tpr *= 2)
+    if (vecs <= tpr) return {tpr, 1};
+  if (vec == 1) {
+    for (int nv : {1, 2, 4})
+      if (vecs <= 128 * nv) return {128, nv};
+    for (int nv : {2, 4, 8, 16})
+      if (vecs <= 512 * nv) return {512, nv};
+    return {512, 32};
+  }
+  for (int tpr = 32; tpr <= 512; tpr *= 2)
+    if (vecs <= 2 * tpr) return {tpr, 2};
+  for (int nv : {3, 4})
+    if (vecs <= 512 * nv) return {512, nv};
+  return {512, 8};
 }
 
-// Backward: two vectors a thread where a row takes several warps, which halves
-// the exchanges and keeps enough loads in flight.
-inline RowShape row_shape_bwd(int vecs) {
-  const RowShape f = row_shape(vecs);
-  return f.tpr > 32 && f.nv == 1 ? RowShape{f.tpr / 2, 2} : f;
-}
-
-#define KDA_NORM_SHAPES(CASE) \
-  CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(64, 1) CASE(128, 1) CASE(256, 1) CASE(512, 1) CASE(512, 2) CASE(512, 3) \
-  CASE(512, 4)
-#define KDA_NORM_SHAPES_BWD(CASE) \
-  CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(32, 2) CASE(64, 2) CASE(128, 2) CASE(256, 2) CASE(512, 2) CASE(512, 3) \
-  CASE(512, 4)
-#define KDA_NORM_SHAPES_LONG(CASE) CASE(512, 8)
-#define KDA_NORM_SHAPES_SCALAR(CASE) CASE(512, 16) CASE(512, 32)
+#define KDA_NORM_SMALL(CASE) CASE(8, 1) CASE(16, 1) CASE(32, 1)
+#define KDA_NORM_LONG(CASE) CASE(512, 3) CASE(512, 4)
+#define KDA_NORM_FWD_WIDE(CASE) \
+  KDA_NORM_SMALL(CASE) CASE(64, 1) CASE(128, 1) CASE(128, 2) CASE(256, 2) CASE(512, 2) KDA_NORM_LONG(CASE)
+#define KDA_NORM_FWD_SCALAR(CASE)                                                                                  \
+  KDA_NORM_SMALL(CASE) CASE(128, 1) CASE(128, 2) CASE(128, 5) CASE(128, 10) CASE(128, 16) CASE(512, 8) CASE(512, 16) \
+  CASE(512, 32)
+#define KDA_NORM_BWD_WIDE(CASE) \
+  KDA_NORM_SMALL(CASE) CASE(32, 2) CASE(64, 2) CASE(128, 2) CASE(256, 2) CASE(512, 2) KDA_NORM_LONG(CASE)
+#define KDA_NORM_BWD_SCALAR(CASE)                                                                                   \
+  KDA_NORM_SMALL(CASE) CASE(128, 1) CASE(128, 2) CASE(128, 4) CASE(512, 2) CASE(512, 4) CASE(512, 8) CASE(512, 16)    \
+  CASE(512, 32)
 
 // Turns of the forward's small rows: the set-up of a thread is worth several
 // rows, as long as every SM keeps about 32 CTAs' worth of them.
@@ -487,7 +518,7 @@ inline int fwd_turns(long long rows, int rows_a_turn) {
 
 template <typename T, int VEC, int QUANT>
 cudaError_t launch_fwd(FwdArgs a, cudaStream_t st) {
-  const RowShape sh = row_shape(a.D / VEC);
+  const RowShape sh = row_shape(a.D / VEC, VEC);
   a.groups = QUANT >= kGroup ? a.D / a.group : 1;
 #define KDA_CASE(TPR, NV)                                                                               \
   if (sh.tpr == TPR && sh.nv == NV) {                                                                    \
@@ -497,9 +528,12 @@ cudaError_t launch_fwd(FwdArgs a, cudaStream_t st) {
     kda_rms_norm_fwd_kernel<T, VEC, TPR, NV, QUANT><<<(unsigned)((a.rows + per - 1) / per), NT, 0, st>>>(a); \
     return cudaGetLastError();                                                                            \
   }
-  KDA_NORM_SHAPES(KDA_CASE)
-  if constexpr (VEC < 8) { KDA_NORM_SHAPES_LONG(KDA_CASE) }
-  if constexpr (VEC == 1) { KDA_NORM_SHAPES_SCALAR(KDA_CASE) }
+  if constexpr (VEC == 1) {
+    KDA_NORM_FWD_SCALAR(KDA_CASE)
+  } else {
+    KDA_NORM_FWD_WIDE(KDA_CASE)
+    if constexpr (VEC < 8) { KDA_CASE(512, 8) }
+  }
 #undef KDA_CASE
   return cudaErrorInvalidValue;
 }
@@ -517,8 +551,8 @@ cudaError_t launch_fwd_groups(const FwdArgs& a, cudaStream_t st) {
 
 // Lines of partial sums of the backward: one per CTA, as many CTAs as run at
 // once (512 threads an SM).
-inline int bwd_grid(long long rows, int vecs) {
-  const RowShape sh = row_shape_bwd(vecs);
+inline int bwd_grid(long long rows, int vecs, int vec) {
+  const RowShape sh = row_shape_bwd(vecs, vec);
   const int nt = threads_of(sh.tpr), rpc = nt / sh.tpr;
   const long long want = (rows + rpc - 1) / rpc, most = 148LL * (512 / nt);
   return (int)(want < most ? want : most);
@@ -526,8 +560,8 @@ inline int bwd_grid(long long rows, int vecs) {
 
 template <typename T, int VEC>
 cudaError_t launch_bwd(const BwdArgs& a, float* dweight, cudaStream_t st) {
-  const RowShape sh = row_shape_bwd(a.D / VEC);
-  const int grid = bwd_grid(a.rows, a.D / VEC);
+  const RowShape sh = row_shape_bwd(a.D / VEC, VEC);
+  const int grid = bwd_grid(a.rows, a.D / VEC, VEC);
   cudaError_t e = cudaErrorInvalidValue;
 #define KDA_CASE(TPR, NV)                                                                          \
   if (sh.tpr == TPR && sh.nv == NV) {                                                               \
@@ -544,9 +578,12 @@ cudaError_t launch_bwd(const BwdArgs& a, float* dweight, cudaStream_t st) {
     kda_rms_norm_bwd_kernel<T, VEC, TPR, NV><<<grid, threads_of(TPR), bytes, st>>>(a);                \
     e = cudaGetLastError();                                                                           \
   }
-  KDA_NORM_SHAPES_BWD(KDA_CASE)
-  if constexpr (VEC < 8) { KDA_NORM_SHAPES_LONG(KDA_CASE) }
-  if constexpr (VEC == 1) { KDA_NORM_SHAPES_SCALAR(KDA_CASE) }
+  if constexpr (VEC == 1) {
+    KDA_NORM_BWD_SCALAR(KDA_CASE)
+  } else {
+    KDA_NORM_BWD_WIDE(KDA_CASE)
+    if constexpr (VEC < 8) { KDA_CASE(512, 8) }
+  }
 #undef KDA_CASE
   if (e != cudaSuccess) return e;
   return launch_sum_lines(a.partial, dweight, nullptr, a.D, grid, a.D, st);
