@@ -351,9 +351,35 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
     return acc.x + acc.y;
   };
 
+  // What the lane prepares of a step whose inputs lie at in[.][s0 ..]: time steps, inputs, and the gate (kForward) or
+  // dy times it (kLocalBwd).  No branch: it runs between the tokens of the step before.
+  float xn[OWN], dn[OWN], gn[OWN];
+  auto prepare = [&](const T(*in)[kTile][CH], int s0) {
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) dn[j] = to_f32<T>(in[1][s0 + own0 + j][ch]) + bias;
+#pragma unroll
+    for (int j = 0; j < OWN; j += 2) {
+      const float2 d2 = softplus2(make_float2(dn[j], dn[OWN > 1 ? j + 1 : j]));
+      dn[j] = d2.x;
+      if (OWN > 1) dn[OWN > 1 ? j + 1 : j] = d2.y;
+    }
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      xn[j] = to_f32<T>(in[0][s0 + own0 + j][ch]);
+      gn[j] = 1.f;
+      if constexpr (kZ) {
+        const float zz = to_f32<T>(in[kZ ? 2 : 0][s0 + own0 + j][ch]);  // anything without a gate
+        const float g = zz * fast_sigmoid(zz);
+        gn[j] = gated ? g : 1.f;
+      }
+      if constexpr (MODE == kLocalBwd) gn[j] *= to_f32<T>(in[MODE == kLocalBwd ? 3 : 0][s0 + own0 + j][ch]);
+    }
+  };
+
   copy_async_wait<1>();
   __syncthreads();
   convert(0, 0);
+  prepare(sm.in[0], 0);  // rows past the chunk's end are prepared from anything and not used
   int buf = 0, st = 0;
   for (long long t = t0; t < t1; t += kTile) {
     copy_async_wait<0>();  // the next tile's copies of this thread
@@ -374,33 +400,23 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
     for (int s0 = 0; s0 < kTile && t + s0 < t1; s0 += kStep) {
       const long long ts = t + s0;
       if (ts == end) next_sequence(ts);  // the first token of another sequence
+      const T(*in_next)[kTile][CH] = s0 + kStep < kTile ? in : sm.in[st1];
+      const int s_next = s0 + kStep < kTile ? s0 + kStep : 0;
       // a final state's gradient is added at its sequence's last token, so that step goes token by token too
       if (ts + kStep <= t1 && (ts >= end || ts + kStep + (MODE == kLocalBwd) <= end)) {
-        float xv[OWN], gv[OWN], dv[OWN];
-#pragma unroll
-        for (int j = 0; j < OWN; ++j) dv[j] = to_f32<T>(in[1][s0 + own0 + j][ch]) + bias;
-#pragma unroll
-        for (int j = 0; j < OWN; j += 2) {
-          const float2 d2 = softplus2(make_float2(dv[j], dv[OWN > 1 ? j + 1 : j]));
-          dv[j] = d2.x;
-          if (OWN > 1) dv[OWN > 1 ? j + 1 : j] = d2.y;
-        }
         __syncwarp();  // the step before has been read
+        float xv[OWN], gv[OWN];
 #pragma unroll
         for (int j = 0; j < OWN; ++j) {
           const int i = own0 + j;
-          xv[j] = to_f32<T>(in[0][s0 + i][ch]);
-          gv[j] = 1.f;
-          if (gated) {
-            const float zz = to_f32<T>(in[kZ ? 2 : 0][s0 + i][ch]);
-            gv[j] = zz * fast_sigmoid(zz);
-          }
-          if constexpr (MODE == kLocalBwd)
-            sm.gv[MODE == kLocalBwd ? i : 0][ch] = gv[j] * to_f32<T>(in[MODE == kLocalBwd ? 3 : 0][s0 + i][ch]);
-          sm.du[i][ch] = make_float4(dv[j], dv[j], dv[j] * xv[j], dv[j] * xv[j]);
-          sumd += dv[j];
+          xv[j] = xn[j];
+          gv[j] = gn[j];
+          sm.du[i][ch] = make_float4(dn[j], dn[j], dn[j] * xn[j], dn[j] * xn[j]);
+          if constexpr (MODE == kLocalBwd) sm.gv[MODE == kLocalBwd ? i : 0][ch] = gn[j];
+          sumd += dn[j];
         }
         __syncwarp();
+        prepare(in_next, s_next);
         float yv[kStep];
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
@@ -439,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
             if (active && sl == 0) yp[(long long)(i - own0) * a.d] = from_f32<T>(fmaf(Dc, xv, y) * gv);
           }
         }
+        prepare(in_next, s_next);
       }
       if (MODE == kForward) yp += (long long)kStep * a.d;
     }

@@ -121,11 +121,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
 #pragma unroll
   for (int k = 0; k < kRun; ++k) accB[k][0] = accB[k][1] = accC[k][0] = accC[k][1] = dup2(0.f);
 
-  // Offsets within the group (the last channel again past its end): the lane's four states in step `step` of the slab
-  // at channel slab0, and the element that this thread chains.
+  // The lane's four states in step `step` of the slab at channel slab0, as an offset within the group (the last channel
+  // again past its end), and what enters the tile at the element that this thread chains.
   auto lane_row = [&](int slab0, int step) { return min(slab0 + step * CPW + chl, a.cpg - 1) * S + sl * 4; };
-  auto chain_row = [&](int slab0, int step) {
-    return min(slab0 + step * CPW + (tid & 127) / S, a.cpg - 1) * S + (tid & 127) % S;
+  auto chain_load = [&](const float* src, int slab0, int step) {  // (nothing enters past the group's end)
+    const int cin = slab0 + step * CPW + (tid & 127) / S;
+    return cin < a.cpg ? src[cin * S + (tid & 127) % S] : 0.f;
   };
   const float* Ag = a.A + gch * S;
   const float* S0g = a.S0 ? a.S0 + gch * S : nullptr;
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
   stage_slab(0);
   // of the step to come
   float4 A4 = *reinterpret_cast<const float4*>(Ag + lane_row(cbl * o.slabs * kSlab, 0));
-  float chained = chain_src[chain_row(cbl * o.slabs * kSlab, 0)];
+  float chained = chain_load(chain_src, cbl * o.slabs * kSlab, 0);
 
   for (int slab = 0; slab < o.slabs; ++slab) {
     const int slab0 = (cbl * o.slabs + slab) * kSlab;  // first channel of the slab in the group
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
         }
         // (the next slab's first step follows the last one; past the block it is read and not used)
         A4 = *reinterpret_cast<const float4*>(Ag + lane_row(slab0, step + 1));
-        chained = chain_src[chain_row(slab0, step + 1)];
+        chained = chain_load(chain_src, slab0, step + 1);
         if (step > 0 && tid >= kBwdThreads - 128) {
           const int cch = slab0 + (step - 1) * CPW + i / S;
           float sum = 0.f;

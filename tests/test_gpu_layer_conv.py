@@ -185,3 +185,34 @@ def test_more_than_2_to_the_31_elements(cuda_device):
     assert torch.equal(y[:, -37:], y2) and torch.equal(s, s2) and torch.count_nonzero(y[:, :-37].view(-1)[::4099]) == 0
     a, b = kda.short_conv_bwd(x, w, x), kda.short_conv_bwd(tail, w, tail)
     assert torch.equal(a["dx"][:, -37:], b["dx"]) and rel_rms(a["dweight"], b["dweight"].cpu()) <= 1e-6
+
+
+@pytest.mark.parametrize("D,W,dtype", [(8, 4, "bf16"), (20, 3, "f32"), (33, 4, "bf16")])
+def test_long_runs(cuda_device, D, W, dtype):
+    """Runs of many groups of tokens, sequences that end anywhere in them (the
+    64-bit form on the device, by shifted products)."""
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(D)
+    lens = [int(n) for n in torch.randint(0, 900, (70,), generator=g)] + [40000]
+    d = _inputs(cuda_device, lens, D, W, dt, 5, True, True)
+    dy = torch.randn(d["x"].shape, device=cuda_device)
+    dstate = torch.randn(len(lens), W - 1, D, device=cuda_device)
+    y, so = kda.short_conv_fwd(d["x"], d["weight"], d["bias"], d["state"], d["cu"])
+    out = kda.short_conv_bwd(d["x"], d["weight"], dy, d["bias"], d["state"], dstate, d["cu"])
+    assert kda.device_error() == 0
+    x, st = d["x"][0].to(F64).requires_grad_(True), d["state"].to(F64).requires_grad_(True)
+    w, b = d["weight"].to(F64).requires_grad_(True), d["bias"].to(F64).requires_grad_(True)
+    ys, ss, at = [], [], 0
+    for n, length in enumerate(lens):
+        rows = torch.cat([st[n], x[at:at + length]])
+        at += length
+        ys.append(R.silu(sum(rows[j:j + length] * w[:, j] for j in range(W)) + b))
+        ss.append(rows[length:])
+    ry, rs = torch.cat(ys), torch.stack(ss)
+    ((ry * dy[0].to(F64)).sum() + (rs * dstate.to(F64)).sum()).backward()
+    assert torch.equal(so.to(F64), rs.detach())
+    # |p| is at most 16 here or so: 2^-21 of the sum of sizes and 2^-22 (8 + |p|) of y stay under 2^-17 (1 + |y|)
+    assert bool(((y[0].to(F64) - ry).abs() <= U[dt] * ry.abs() + 2.0 ** -17 * (1 + ry.abs())).all())
+    assert rel_rms(out["dx"][0], x.grad.cpu()) <= U[dt] + 1e-5
+    for name, t in (("dweight", w), ("dbias", b), ("dinit", st)):
+        assert rel_rms(out[name], t.grad.cpu()) <= 2e-5, name

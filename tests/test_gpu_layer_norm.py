@@ -177,3 +177,40 @@ def test_more_than_2_to_the_31_elements(cuda_device):
     q, scale, _ = kda.rms_norm_quant_fwd(x, w, group=128)
     q2, scale2, _ = kda.rms_norm_quant_fwd(tail, w, group=128)
     assert torch.equal(q[-5:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(scale[-5:], scale2)
+
+
+@pytest.mark.parametrize("rows,D,dtype", [(300001, 72, "bf16"), (299999, 50, "bf16"), (160003, 128, "f32"),
+                                          (400000, 17, "f32"), (40001, 500, "bf16")])
+def test_many_rows(cuda_device, rows, D, dtype):
+    """Rows that a thread takes in turns, and the backward's rows over every CTA
+    (the 64-bit form on the device: only its own arithmetic is used)."""
+    dt = DT[dtype]
+    x, w, res = _inputs(cuda_device, rows, D, dt, D, True)
+    y, s = kda.rms_norm_fwd(x, w, res)
+    ry, rs = R.norm(x.to(F64), w.to(F64), res.to(F64))
+    assert bool(((y.to(F64) - ry).abs() <= (U[dt] + K) * ry.abs()).all())
+    assert bool(((s.to(F64) - rs).abs() <= (U[dt] * (1 + 2.0 ** -20) + 2.0 ** -24) * rs.abs()).all())
+    q, scale, _ = kda.rms_norm_quant_fwd(x, w, res)
+    rscale = ry.abs().amax(-1, keepdim=True) / 448
+    assert bool(((scale.to(F64) - rscale).abs() <= 2 * K * rscale).all())
+    v = ry / rscale
+    bound = torch.maximum(v.abs() * 2.0 ** -4, torch.full_like(v, 2.0 ** -10)) + 4 * K * v.abs()
+    assert bool(((q.to(F64) - v).abs() <= bound).all())
+    if D % 32 == 0:
+        q, scale, _ = kda.rms_norm_quant_fwd(x, w, res, group=32)
+        rg = ry.view(rows, -1, 32)
+        rscale = rg.abs().amax(-1) / 448
+        assert bool(((scale.to(F64) - rscale).abs() <= 2 * K * rscale).all())
+    out = kda.rms_norm_bwd(y, s, w, x)
+    sd, g = s.to(F64), y.to(F64)
+    r = 1 / (sd.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    gw = g * w.to(F64)
+    want = r * gw - sd * r ** 3 * (gw * sd).mean(-1, keepdim=True) + x.to(F64)
+    size = (r * gw).abs() + sd.abs() * r ** 3 * (gw * sd).abs().mean(-1, keepdim=True)
+    # dx adds three terms in fp32: its two additions round partial sums that are at most |ds| + size, by half a step
+    # (2^-24) each, whatever is left of them in dx
+    adds = 2 * 2.0 ** -24 * (x.to(F64).abs() + size)
+    assert bool(((out["dx"].to(F64) - want).abs() <= U[dt] * want.abs() + 4 * K * size + adds).all())
+    terms = g * sd * r
+    # a column's sum in fp32: chains of up to rows / 148 additions, each off by 2^-24 of what it holds
+    assert bool(((out["dweight"].to(F64) - terms.sum(0)).abs() <= (2 * K + rows / 148 * 2.0 ** -24) * terms.abs().sum(0)).all())

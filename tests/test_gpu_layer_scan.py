@@ -245,3 +245,43 @@ def test_tokens_behind_the_last_sequence_are_refused(cuda_device):
     v["cu"] = torch.tensor([0, 20, 40], dtype=torch.int32, device=cuda_device)  # 60 tokens given
     _fwd(v)
     assert kda.device_error() == 1
+
+
+@pytest.mark.parametrize("lens,dtype", [((9000,), "f32"), ((2500, 2500, 2500), "bf16"), ((3000, 0, 5000, 700, 1), "f32")])
+def test_long_sequences(cuda_device, lens, dtype):
+    """Chunks of many tiles.  Decays of up to a few thousand tokens' memory
+    (steps of 0.001 to 0.1, A from -1): errors add up over the memory, so the
+    forward's bound is the recurrence's own; the gradients, which sum as many
+    terms, 3e-4 of their root mean square."""
+    packed = len(set(lens)) > 1
+    v = _inputs(cuda_device, lens, 16, 8, 2, DT[dtype], 31, packed)
+    v["dt_bias"] -= 1.5
+    y, So = _fwd(v)
+    assert kda.device_error() == 0
+    _check_fwd(v, lens, y, So)
+    dy, dS = torch.randn_like(v["x"]), torch.randn(len(lens), 16, 8, device=cuda_device)
+    out = _bwd(v, dy, dS)
+    args = _ref_args(v, lens)
+    g = R.grads(lambda **a: R.scan(*a.values(), lens), args, [_c(dy).reshape(args["x"].shape), _c(dS)])
+    for name, key, bf in (("dx", "x", True), ("ddt", "dt", True), ("dz", "z", True), ("dA", "A", False),
+                          ("dB", "B", False), ("dC", "C", False), ("dD", "D", False), ("ddt_bias", "dt_bias", False),
+                          ("dS0", "state", False)):
+        err = rel_rms(out[name].reshape(g[key].shape), g[key])
+        assert err <= 3e-4 + (U[DT[dtype]] if bf else 0), f"{name}: {err:.3e}"
+
+
+def test_nan_in_the_backward_stays_with_its_sequence(cuda_device):
+    """A NaN input of one sequence and channel reaches that sequence's dB, dC and
+    that channel's sums, and nothing of the other sequences."""
+    lens = (70, 90, 60)
+    v = _inputs(cuda_device, lens, 37, 16, 1, torch.float32, 33, True)
+    dy = torch.randn_like(v["x"])
+    ref = _bwd(v, dy, None)
+    v["x"][0, 100, 36] = float("nan")
+    out = _bwd(v, dy, None)
+    other = torch.ones(220, dtype=torch.bool, device=cuda_device)
+    other[70:160] = False
+    for name in ("dx", "ddt", "dz", "dB", "dC"):
+        assert torch.equal(out[name][0][other], ref[name][0][other]), name
+    assert torch.equal(out["dA"][:36], ref["dA"][:36]) and torch.equal(out["dD"][:36], ref["dD"][:36])
+    assert torch.equal(out["dS0"][[0, 2]], ref["dS0"][[0, 2]]) and torch.equal(out["dx"][..., :36], ref["dx"][..., :36])
