@@ -138,6 +138,21 @@ __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
+// max(m, |a|, |b|) that keeps NaN.
+__device__ __forceinline__ float max_abs_nan(float m, float a, float b) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(m), "f"(a), "f"(b));
+  return y;
+}
+// max(m, |x_e|) that keeps NaN; m >= 0.
+template <int N>
+__device__ __forceinline__ float max_abs_nan(float m, const float (&x)[N]) {
+#pragma unroll
+  for (int e = 0; e + 1 < N; e += 2) m = max_abs_nan(m, x[e], x[e + 1]);
+  if (N % 2) m = max_nan(m, fabsf(x[N - 1]));
+  return m;
+}
+
 // Two fp32 lanes in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;

@@ -117,42 +117,44 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
   const int j = threadIdx.x % TPR;
   const int nvec = a.D / VEC;
   const int turns = kTurns ? a.turns : 1;
-  long long row0 = ((long long)blockIdx.x * turns * RPC + threadIdx.x / TPR) * RU;  // the thread's first row
-  const long long step = (long long)RPC * RU;
+  const long long row0 = ((long long)blockIdx.x * turns * RPC + threadIdx.x / TPR) * RU;  // the thread's first row
+  constexpr int kStep = RPC * RU;
+  // rows from row0 on; a turn's rows are counted from it
+  const int left = (int)(a.rows - row0 < (1 << 20) ? a.rows - row0 : (1 << 20));
   const T* xp = static_cast<const T*>(a.x) + row0 * a.x_stride + j * VEC;
   const T* rp = a.residual ? static_cast<const T*>(a.residual) + row0 * a.D + j * VEC : nullptr;
 
   Pack<T, VEC> px[RU][NV], pr[RU][NV];
   // rows past the end are not read and not written
-  auto fetch = [&](long long first) {
+  auto fetch = [&](int first) {
     if constexpr (!kAsync) {
 #pragma unroll
       for (int u = 0; u < RU; ++u)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (first + u < a.rows && j + i * TPR < nvec) {
+          if (first + u < left && j + i * TPR < nvec) {
             px[u][i] = load_pack<T, VEC>(xp + u * a.x_stride + i * TPR * VEC);
             if (rp) pr[u][i] = load_pack<T, VEC>(rp + u * a.D + i * TPR * VEC);
           }
-      xp += step * a.x_stride;
-      if (rp) rp += step * a.D;
+      xp += kStep * a.x_stride;
+      if (rp) rp += (long long)kStep * a.D;
     }
   };
-  int ahead = 0, slot = 0;  // turns staged; the ring's slot to fill
+  int ahead = 0, slot = 0;  // first row to stage; the ring's slot to fill
   auto stage = [&] {
     if constexpr (kAsync) {
-      if (ahead < turns && j < nvec) {
+      if (ahead < turns * kStep && j < nvec) {
 #pragma unroll
         for (int u = 0; u < RU; ++u)
-          if (row0 + ahead * step + u < a.rows) {
+          if (ahead + u < left) {
             copy_async<sizeof(T) * VEC>(&s_in[slot][u][0][threadIdx.x], xp + u * a.x_stride);
             if (rp) copy_async<sizeof(T) * VEC>(&s_in[slot][u][1][threadIdx.x], rp + u * a.D);
           }
       }
       copy_async_commit();
-      xp += step * a.x_stride;
-      if (rp) rp += step * a.D;
-      ++ahead;
+      xp += kStep * a.x_stride;
+      if (rp) rp += (long long)kStep * a.D;
+      ahead += kStep;
       slot = slot + 1 < kRing ? slot + 1 : 0;
     }
   };
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
 #pragma unroll
     for (int g = 0; g < kRing - 1; ++g) stage();
   } else {
-    fetch(row0);
+    fetch(0);
   }
   float w[NV][VEC];
 #pragma unroll
@@ -174,17 +176,13 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
   char* yp = static_cast<char*>(a.y) + (row0 * a.D + j * VEC) * (QUANT == kNone ? sizeof(T) : 1);
   T* sp = a.s ? static_cast<T*>(a.s) + row0 * a.D + j * VEC : nullptr;
   float* scp = QUANT != kNone ? a.scale + row0 * a.groups + (QUANT >= kGroup ? j / GL : 0) : nullptr;
-  const long long first_row = row0;
   int read = 0;
 #pragma unroll 1
-  for (int turn = 0; turn < turns; ++turn) {
-    if (RPC > 1 && row0 - threadIdx.x / TPR * RU >= a.rows) return;  // (uniform: a CTA's slots are consecutive rows)
+  for (int row = 0; row < turns * kStep; row += kStep) {
+    if (RPC > 1 && row >= left + (int)(threadIdx.x / TPR) * RU) return;  // uniform: a CTA's slots are consecutive rows
     float v[RU][NV][VEC], acc[RU];
     if constexpr (kAsync) {
-      const long long at = row0;
-      row0 = first_row;  // stage() counts from the first turn
       stage();
-      row0 = at;
       copy_async_wait<kRing - 1>();
     }
 #pragma unroll
@@ -192,7 +190,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
       acc[u] = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (row0 + u < a.rows && j + i * TPR < nvec) {
+        if (row + u < left && j + i * TPR < nvec) {
           unpack<T, VEC>(kAsync ? s_in[read][kAsync ? u : 0][0][kAsync ? threadIdx.x : 0] : px[u][i], v[u][i]);
           if (rp) {
             float q[VEC];
@@ -208,14 +206,14 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
       }
     }
     if (kAsync) read = read + 1 < kRing ? read + 1 : 0;
-    if (!kAsync && turn + 1 < turns) fetch(row0 + step);
+    if (!kAsync && row + kStep < turns * kStep) fetch(row + kStep);
     if (sp) {
 #pragma unroll
       for (int u = 0; u < RU; ++u)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (row0 + u < a.rows && j + i * TPR < nvec) store_pack<T, VEC>(sp + u * a.D + i * TPR * VEC, v[u][i]);
-      sp += step * a.D;
+          if (row + u < left && j + i * TPR < nvec) store_pack<T, VEC>(sp + u * a.D + i * TPR * VEC, v[u][i]);
+      sp += (long long)kStep * a.D;
     }
     // the sum is taken of the unrounded s (the stored s is rounded once, to T)
     row_reduce<TPR, false>(acc, s_red[0]);
@@ -228,9 +226,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
       for (int i = 0; i < NV; ++i) {
         scale_by<VEC>(v[u][i], r);
         scale_by<VEC>(v[u][i], w[i]);
-        if (QUANT == kRow)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) amax[u] = max_nan(amax[u], fabsf(v[u][i][e]));
+        if (QUANT == kRow) amax[u] = max_abs_nan<VEC>(amax[u], v[u][i]);
       }
     }
     if constexpr (QUANT == kNone) {
@@ -238,22 +234,20 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
       for (int u = 0; u < RU; ++u)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (row0 + u < a.rows && j + i * TPR < nvec)
+          if (row + u < left && j + i * TPR < nvec)
             store_pack<T, VEC>(reinterpret_cast<T*>(yp) + u * a.D + i * TPR * VEC, v[u][i]);
-      yp += step * a.D * sizeof(T);
+      yp += (long long)kStep * a.D * sizeof(T);
     } else {
       if constexpr (QUANT == kRow) row_reduce<TPR, true>(amax, s_red[1]);
 #pragma unroll
       for (int u = 0; u < RU; ++u) {
-        const bool live = row0 + u < a.rows;
+        const bool live = row + u < left;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = j + i * TPR;
           float m = amax[u];
           if constexpr (QUANT >= kGroup) {
-            m = 0.f;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) m = max_nan(m, fabsf(v[u][i][e]));
+            m = max_abs_nan<VEC>(0.f, v[u][i]);
 #pragma unroll
             for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
           }
@@ -271,10 +265,9 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
           }
         }
       }
-      yp += step * a.D;
-      scp += step * a.groups;
+      yp += (long long)kStep * a.D;
+      scp += (long long)kStep * a.groups;
     }
-    row0 += step;
   }
 }
 

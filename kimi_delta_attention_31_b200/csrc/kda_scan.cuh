@@ -481,31 +481,34 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
 __global__ void __launch_bounds__(128) kda_scan_carry_kernel(const float* __restrict__ A, float* entry, float* exitg,
                                                              const float* __restrict__ sumd, int d, int S,
                                                              long long chunks) {
-  constexpr int U = 8;
+  constexpr int U = 16;  // chunks loaded together
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long row = (long long)d * S;
   if (i >= row) return;
   const int c = (int)(i / S);
   const float A2 = A[i] * kLog2eF;
   const bool rev = blockIdx.y == 1;
-  float* v = rev ? exitg : entry;
+  const long long step = rev ? -row : row, dstep = rev ? -d : d;
+  float* v = (rev ? exitg + (chunks - 1) * row : entry) + i;
+  const float* sp = sumd + (rev ? (chunks - 1) * d : 0) + c;
   float h = 0.f;
   for (long long k0 = 0; k0 < chunks; k0 += U) {
+    const int m = chunks - k0 < U ? (int)(chunks - k0) : U;
     float loc[U], sd[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (k0 + u < chunks) {
-        const long long k = rev ? chunks - 1 - k0 - u : k0 + u;
-        loc[u] = v[k * row + i];
-        sd[u] = sumd[k * d + c];
+      if (u < m) {
+        loc[u] = v[u * step];
+        sd[u] = sp[u * dstep];
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (k0 + u < chunks) {
-        const long long k = rev ? chunks - 1 - k0 - u : k0 + u;
-        v[k * row + i] = h;
+      if (u < m) {
+        v[u * step] = h;
         h = sd[u] < 0.f ? loc[u] : fmaf(ex2(fmaf(sd[u], A2, kEx2Bias)), h, loc[u]);
       }
+    v += U * step;
+    sp += U * dstep;
   }
 }
 
