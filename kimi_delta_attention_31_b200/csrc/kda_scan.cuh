@@ -158,7 +158,7 @@ struct alignas(16) TileSmem {
   static constexpr bool kConvert = sizeof(T) != 4;  // fp32 ones are read where they are
   float B[2][kConvert ? kTile : 1][kConvert ? S : 4];
   float C[2][kConvert && MODE != 1 ? kTile : 1][kConvert && MODE != 1 ? S : 4];
-  float4 du[kStep][CH];                         // delta twice, delta x twice
+  float2 du[kStep][CH];                         // delta, delta x (each once: what lanes read bounds the kernel too)
   float gv[MODE == 2 ? kStep : 1][CH];          // dy silu(z)
 };
 
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
           const int i = own0 + j;
           xv[j] = xn[j];
           gv[j] = gn[j];
-          sm.du[i][ch] = make_float4(dn[j], dn[j], dn[j] * xn[j], dn[j] * xn[j]);
+          sm.du[i][ch] = make_float2(dn[j], dn[j] * xn[j]);
           if constexpr (MODE == kLocalBwd) sm.gv[MODE == kLocalBwd ? i : 0][ch] = gn[j];
           sumd += dn[j];
         }
@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
         float yv[kStep];
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
-          const float4 du = sm.du[i][ch];
-          yv[i] = token(make_float2(du.x, du.y), make_float2(du.z, du.w), MODE == kLocalBwd ? sm.gv[MODE == kLocalBwd ? i : 0][ch] : 0.f, Bt + (s0 + i) * S,
+          const float2 du = sm.du[i][ch];
+          yv[i] = token(dup2(du.x), dup2(du.y), MODE == kLocalBwd ? sm.gv[MODE == kLocalBwd ? i : 0][ch] : 0.f, Bt + (s0 + i) * S,
                         Ct + (s0 + i) * S, false);
         }
         if constexpr (MODE == kForward) {

@@ -56,8 +56,8 @@ template <typename T, int S>
 struct alignas(16) BwdSmem {
   T in[2][4][kTokens][kSlab];  // x, dt, dy, z as they are in memory: this slab's and the next one's
   float B[kTokens][S], C[kTokens][S];
-  float4 du[kTokens][kSlab];   // delta twice, delta x twice
-  float2 dyy[kTokens][kSlab];  // twice
+  float2 du[kTokens][kSlab];   // delta, delta x (each once: what lanes read bounds the kernel too)
+  float dyy[kTokens][kSlab];
   float sA[kTokens][kSlab], gB[kTokens][kSlab], yy[kTokens][kSlab];
   float P[kWarps][128], H[kWarps][128], R[kWarps][128], dA[2][kWarps][128];
   float ch[kWarps][2][kSlab];
@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
           g *= zz * fast_sigmoid(zz);
         }
         const float u = ok ? delta * to_f32<T>(in[0][t][lane]) : 0.f;
-        s.du[t][lane] = make_float4(delta, delta, u, u);
-        s.dyy[t][lane] = make_float2(g, g);
+        s.du[t][lane] = make_float2(delta, u);
+        s.dyy[t][lane] = g;
       }
     }
     __syncwarp();
@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
           const int t = tw + k;
-          const float4 du = s.du[t][ch];
-          const float2 gy = s.dyy[t][ch];
+          const float2 dux = s.du[t][ch];
+          const float4 du = make_float4(dux.x, dux.x, dux.y, dux.y);
+          const float2 gy = dup2(s.dyy[t][ch]);
           const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
           const float4 c4 = *reinterpret_cast<const float4*>(&s.C[t][sl * 4]);
           da[k][0] = decay2(lo2(du), A2[0]);
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
             hin[k][0] = h0;
             hin[k][1] = h1;
             if (k + 1 < kRun) {
-              const float2 u = hi2(s.du[t][ch]);
+              const float2 u = dup2(s.du[t][ch].y);
               const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
               h0 = fma2(da[k][0], h0, mul2(u, lo2(b4)));
               h1 = fma2(da[k][1], h1, mul2(u, hi2(b4)));
@@ -299,8 +300,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
 #pragma unroll
           for (int kk = BT - 1; kk >= 0; --kk) {
             const int k = kb * BT + kk, t = tw + k;
-            const float4 du = s.du[t][ch];
-            const float2 gy = s.dyy[t][ch], u = hi2(du);
+            const float2 dux = s.du[t][ch];
+            const float4 du = make_float4(dux.x, dux.x, dux.y, dux.y);
+            const float2 gy = dup2(s.dyy[t][ch]), u = hi2(du);
             const float4 b4 = *reinterpret_cast<const float4*>(&s.B[t][sl * 4]);
             const float4 c4 = *reinterpret_cast<const float4*>(&s.C[t][sl * 4]);
             if (kEdges && s.last[t] >= 0) {  // what comes from the right is the final state's gradient
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
           const long long t = t0 + tw + k;
           const float xv = to_f32<T>(in[0][tw + k][lane]);
           const float raw = to_f32<T>(in[1][tw + k][lane]) + bias;
-          const float delta = s.du[tw + k][lane].x, gy = s.dyy[tw + k][lane].x, gb = s.gB[tw + k][lane];
+          const float delta = s.du[tw + k][lane].x, gy = s.dyy[tw + k][lane], gb = s.gB[tw + k][lane];
           const float ddelta = fmaf(gb, xv, s.sA[tw + k][lane] * kLn2F);
           const float ddt = ddelta * fast_sigmoid(raw);
           static_cast<T*>(o.dx)[t * a.d + c] = from_f32<T>(fmaf(gb, delta, Dc * gy));
