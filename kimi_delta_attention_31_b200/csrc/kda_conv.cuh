@@ -15,8 +15,8 @@
 // copies in groups of kGroup, a few groups ahead, in a ring in shared memory that
 // each thread has to itself (no barrier; loads ahead in registers left too few
 // threads on an SM: 316 us for 65536 tokens of 4096 channels, 52% of the copy
-// rate; through the ring 186 us, 5.8 TB/s, 89%).  The backward reads x and dy once
-// and writes dx: 118 us for 16384 tokens (4.5 TB/s; its arithmetic and the sum of
+// rate; through the ring 186 to 197 us, 5.5 TB/s and more).  The backward reads x and dy once
+// and writes dx: 117 us for 16384 tokens (4.6 TB/s; its arithmetic and the sum of
 // the weights' lines show); the step, 256 sequences of 12288 channels, 11 us
 // (4.6 TB/s).  Products and sums are fp32, two at a time; the output is rounded once.
 #pragma once
@@ -464,9 +464,10 @@ inline long long fwd_run(long long tokens, int ncol) {
   return (L + kGroup - 1) / kGroup * kGroup;
 }
 // Backward runs: every run writes a line of partial sums, so no more of them
-// than fill the card (six CTAs an SM), none under 16 tokens.
+// than run at once (four CTAs an SM; six: 123.6 us against 117.0 for 16384
+// tokens of 4096 channels), none under 16 tokens.
 inline long long bwd_run(long long tokens, int ncol) {
-  long long L = (tokens * ncol + 148 * 6 - 1) / (148 * 6);
+  long long L = (tokens * ncol + 148 * 4 - 1) / (148 * 4);
   L = L < 16 ? 16 : L;
   return (L + kGroup - 1) / kGroup * kGroup;
 }
