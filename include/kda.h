@@ -343,8 +343,9 @@ kda_status_t kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, 
  *     malformed table raises the device error word (kda_device_error reports
  *     KDA_ERR_INVALID_ARG); no read or write leaves the buffers' bounds, and
  *     the outputs are then unspecified.  Sequences may be empty.
- *   - Outputs must not alias inputs unless stated.  Results do not depend on
- *     scheduling: no floating-point atomics.
+ *   - Outputs must not alias inputs unless stated.  A workspace is scratch of one
+ *     call: calls whose executions overlap need one each.  Results do not depend
+ *     on scheduling: no floating-point atomics.
  */
 
 /*

@@ -160,14 +160,14 @@ __global__ void __launch_bounds__(kThreads, 4) kda_short_conv_fwd_kernel(const F
   if (blockIdx.x == 0) check_seq_table(a.q);
   if (c0 >= a.D) return;
   T* state_out = static_cast<T*>(a.state_out);
-  if (run == 0 && state_out) {  // sequences without tokens keep their state
-    for (int n = 0; n < a.q.num; ++n)
-      if (seq_empty(a.q, n)) {
+  if (state_out && may_have_empty(a.q)) {  // sequences without tokens keep their state: every run looks at some
+    for (long long n = run; n < a.q.num; n += gridDim.x / a.ncol)
+      if (seq_empty(a.q, (int)n)) {
 #pragma unroll
         for (int r = 0; r < W - 1; ++r) {
           float v[VEC];
-          load_state_row<T, VEC, W>(a.state, n, r, a.D, c0, v);
-          store_pack<T, VEC>(state_out + ((long long)n * (W - 1) + r) * a.D + c0, v);
+          load_state_row<T, VEC, W>(a.state, (int)n, r, a.D, c0, v);
+          store_pack<T, VEC>(state_out + (n * (W - 1) + r) * a.D + c0, v);
         }
       }
   }
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_short_conv_fwd_kernel(const F
         const long long ti = t + i;
         if (decltype(plain)::value || ti < t1) {
           if (!decltype(plain)::value && ti == end) {  // the first token of another sequence
-            n = seq_of_token(a.q, ti);
+            n = next_seq(a.q, n, ti);
             end = seq_end(a.q, n);
 #pragma unroll
             for (int r = 0; r < W - 1; ++r) load_state_row<T, VEC, W>(a.state, n, r, a.D, c0, xs[i + r]);
@@ -307,9 +307,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_short_conv_bwd_kernel(const B
   const int c0 = (col * kThreads + (int)threadIdx.x) * VEC;
   if (blockIdx.x == 0) check_seq_table(a.q);
   if (c0 >= a.D) return;
-  if (run == 0 && a.dinit) {  // sequences without tokens: the state out is the state
-    for (int n = 0; n < a.q.num; ++n)
-      if (seq_empty(a.q, n)) {
+  if (a.dinit && may_have_empty(a.q)) {  // sequences without tokens: the state out is the state
+    for (long long n = run; n < a.q.num; n += gridDim.x / a.ncol)
+      if (seq_empty(a.q, (int)n)) {
 #pragma unroll
         for (int r = 0; r < W - 1; ++r) {
           const long long at = ((long long)n * (W - 1) + r) * a.D + c0;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_short_conv_bwd_kernel(const B
           const long long ti = t + i;
           if (kPlain || ti < t1) {
             if (!kPlain && ti == end) {
-              n = seq_of_token(a.q, ti);
+              n = next_seq(a.q, n, ti);
               start = seq_start(a.q, n);
               end = seq_end(a.q, n);
 #pragma unroll

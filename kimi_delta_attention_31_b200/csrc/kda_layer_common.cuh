@@ -87,6 +87,16 @@ __device__ __forceinline__ long long seq_start(const Seqs& q, int n) { return q.
 __device__ __forceinline__ long long seq_end(const Seqs& q, int n) {
   return q.cu ? (long long)q.cu[n + 1] : (n + 1) * q.T;
 }
+// The sequence of token t where sequence n has just ended there: the next one
+// with tokens.  In [0, num) whatever the table holds.
+__device__ __forceinline__ int next_seq(const Seqs& q, int n, long long t) {
+  int m = n + 1 < q.num ? n + 1 : q.num - 1;
+  if (q.cu)
+    while (m + 1 < q.num && (long long)q.cu[m + 1] <= t) ++m;
+  return m;
+}
+// Whether a call can have sequences without tokens.
+__device__ __forceinline__ bool may_have_empty(const Seqs& q) { return q.cu || q.T == 0; }
 __device__ __forceinline__ bool seq_empty(const Seqs& q, int n) { return seq_end(q, n) <= seq_start(q, n); }
 
 // Raises the device error word if the packed table is not 0 .. total,

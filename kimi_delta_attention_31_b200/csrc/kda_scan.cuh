@@ -236,13 +236,13 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   const long long crow = c * S + sl * 4;
 
   if (blockIdx.x == 0) check_seq_table(a.q);
-  if (MODE == kForward && chunk == 0 && a.S_out) {  // sequences without tokens keep their state
-    for (int n = 0; n < a.q.num; ++n)
-      if (seq_empty(a.q, n) && active) {
+  if (MODE == kForward && a.S_out && may_have_empty(a.q)) {  // sequences without tokens keep their state
+    for (long long n = chunk; n < a.q.num; n += a.chunks)
+      if (seq_empty(a.q, (int)n) && active) {
         float2 v[NP];
-        if (a.S0) load_state<NP, LPC * 4>(a.S0 + (long long)n * a.d * S + crow, v);
+        if (a.S0) load_state<NP, LPC * 4>(a.S0 + n * a.d * S + crow, v);
         else zero_state<NP>(v);
-        store_state<NP, LPC * 4>(a.S_out + (long long)n * a.d * S + crow, v);
+        store_state<NP, LPC * 4>(a.S_out + n * a.d * S + crow, v);
       }
   }
   const long long t0 = chunk * a.L;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
 
   auto next_sequence = [&](long long t) {
     if (MODE == kForward && a.S_out && active) store_state<NP, LPC * 4>(a.S_out + (long long)n * a.d * S + crow, h);
-    n = seq_of_token(a.q, t);
+    n = next_seq(a.q, n, t);
     end = seq_end(a.q, n);
     cut = true;
     if (a.S0) load_state<NP, LPC * 4>(a.S0 + (long long)n * a.d * S + crow, h);

@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
 // dS0 of sequences without tokens: what comes from the right passes.
 __global__ void __launch_bounds__(256) kda_scan_empty_bwd_kernel(const Seqs q, const float* dS, float* dS0,
                                                                  long long row) {
+  if (blockIdx.x == 0) check_seq_table(q);
   for (int n = blockIdx.x; n < q.num; n += gridDim.x)
     if (seq_empty(q, n))
       for (long long i = threadIdx.x; i < row; i += blockDim.x) dS0[n * row + i] = dS ? dS[n * row + i] : 0.f;

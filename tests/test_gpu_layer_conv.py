@@ -216,3 +216,22 @@ def test_long_runs(cuda_device, D, W, dtype):
     assert rel_rms(out["dx"][0], x.grad.cpu()) <= U[dt] + 1e-5
     for name, t in (("dweight", w), ("dbias", b), ("dinit", st)):
         assert rel_rms(out[name], t.grad.cpu()) <= 2e-5, name
+
+
+def test_many_short_sequences(cuda_device):
+    g = torch.Generator().manual_seed(3)
+    lens = [int(n) for n in torch.randint(0, 6, (700,), generator=g)] + [0, 0, 90, 0]
+    d = _inputs(cuda_device, lens, 24, 4, torch.float32, 17)
+    dy, dstate = torch.randn(d["x"].shape, device=cuda_device), torch.randn(len(lens), 3, 24, device=cuda_device)
+    y, so = kda.short_conv_fwd(d["x"], d["weight"], d["bias"], d["state"], d["cu"])
+    out = kda.short_conv_bwd(d["x"], d["weight"], dy, d["bias"], d["state"], dstate, d["cu"])
+    assert kda.device_error() == 0
+    ry, rs = R.conv(_flat(d["x"]), _c(d["weight"]), _c(d["bias"]), _c(d["state"]), lens)
+    assert torch.equal(_c(so), rs)
+    p, size = _p_size(d, lens)
+    within(y[0], ry, U[torch.float32] * ry.abs() + 1.1 * 2.0 ** -21 * size + 2.0 ** -22 * (8 + p.abs()) * ry.abs())
+    gr = R.grads(lambda x, weight, bias, state: R.conv(x, weight, bias, state, lens),
+                 dict(x=_flat(d["x"]), weight=_c(d["weight"]), bias=_c(d["bias"]), state=_c(d["state"])),
+                 [_flat(dy), _c(dstate)])
+    for name, key in (("dx", "x"), ("dweight", "weight"), ("dbias", "bias"), ("dinit", "state")):
+        assert rel_rms(out[name].reshape(gr[key].shape), gr[key]) <= 1e-5, name

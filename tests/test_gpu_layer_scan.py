@@ -285,3 +285,23 @@ def test_nan_in_the_backward_stays_with_its_sequence(cuda_device):
         assert torch.equal(out[name][0][other], ref[name][0][other]), name
     assert torch.equal(out["dA"][:36], ref["dA"][:36]) and torch.equal(out["dD"][:36], ref["dD"][:36])
     assert torch.equal(out["dS0"][[0, 2]], ref["dS0"][[0, 2]]) and torch.equal(out["dx"][..., :36], ref["dx"][..., :36])
+
+
+def test_many_short_sequences_and_more_than_a_grid_dimension_of_steps(cuda_device):
+    g = torch.Generator().manual_seed(3)
+    lens = [int(n) for n in torch.randint(0, 6, (500,), generator=g)] + [0, 0, 40, 0]
+    v = _inputs(cuda_device, lens, 12, 8, 1, torch.float32, 41, True)
+    y, So = _fwd(v)
+    assert kda.device_error() == 0
+    _check_fwd(v, lens, y, So)
+    dy, dS = torch.randn_like(v["x"]), torch.randn(len(lens), 12, 8, device=cuda_device)
+    _check_bwd(v, lens, _bwd(v, dy, dS), dy, dS)
+    N = 65536 + 5  # the step's sequences lie along a grid dimension of 65535
+    w = _inputs(cuda_device, [1] * N, 2, 8, 1, torch.float32, 42, False)
+    row = {k: (t[:, 0] if k in ("x", "dt", "z", "B", "C") else t) for k, t in w.items()}
+    keep = w["S0"].clone()
+    y = kda.selective_scan_step(row["x"], row["dt"], w["A"], row["B"], row["C"], w["S0"], w["D"], row["z"], w["dt_bias"])
+    at = [0, 1, 65534, 65535, 65536, N - 1]
+    sub = {k: (t[at] if k in ("x", "dt", "z", "B", "C") else t) for k, t in w.items()}
+    sub["S0"] = keep[at]
+    _check_fwd(sub, [1] * len(at), y[at], w["S0"][at])
