@@ -616,10 +616,12 @@ inline int channel_blocks(int d, int groups, int S) {
   return groups * ((d / groups + ch - 1) / ch);
 }
 
-// Chunks of the forward.  A batch whose channels give every SM sub-partition a
-// warp or more runs unsplit (a split costs the exponentials a second time);
-// otherwise, and for packed sequences, the token axis is cut so that about
-// 16 warps an SM run at once, into chunks of 64 tokens at least.
+// Chunks of the forward.  A split costs the exponentials a second time, a batch
+// without one leaves SMs idle: 4096 tokens of 1024 channels (64 warps a row), split
+// and unsplit: 4 rows 228 and 461 us, 8 rows 409 and 455, 12 rows 588 and 586, 16
+// rows 760 and 585.  So a batch with a warp or more for every SM sub-partition runs
+// unsplit; others, and packed sequences, have the token axis cut so that about 16
+// warps an SM run at once, into chunks of 64 tokens at least.
 struct FwdPlan {
   bool split;
   long long L, chunks;
@@ -641,7 +643,7 @@ inline FwdPlan fwd_plan(long long B, long long T, int num_seqs, int d, int group
   const long long tokens = B * T;
   const long long warps = (long long)channel_blocks(d, groups, S) * (kThreads / 32);
   const bool packed = num_seqs > 1;
-  if (!packed && (B * warps >= 148 * 8 || T < 128)) return {false, T > 0 ? T : 1, B};
+  if (!packed && (B * warps >= 148 * 4 || T < 128)) return {false, T > 0 ? T : 1, B};
   if (tokens < 128) return {false, tokens > 0 ? tokens : 1, 1};
   long long chunks = 148 * 16 / warps;
   if (chunks < 1) chunks = 1;
