@@ -176,7 +176,24 @@ struct alignas(16) TileSmem {
 template <typename T, int WIDTH, int THREADS>
 __device__ __noinline__ void stage_rows_narrow(T (*dst)[WIDTH], const T* src, long long stride, int rows, int len,
                                                int bytes) {
-  const int shift = bytes == 8 ? (sizeof(T) == 2 ? 2 : 1) : bytes == 4 && sizeof(T) == 2 ? 1 : 0;  // elements: 1 << shift
+  if (bytes == 0) {  // element by element, eight loads at a time
+    constexpr int U = 8;
+    for (int e0 = threadIdx.x; e0 < rows * WIDTH; e0 += U * THREADS) {
+      T v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int e = e0 + i * THREADS, r = e / WIDTH, k = e % WIDTH;
+        if (r < rows && k < len) v[i] = src[r * stride + k];
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int e = e0 + i * THREADS, r = e / WIDTH, k = e % WIDTH;
+        if (r < rows && k < len) dst[r][k] = v[i];
+      }
+    }
+    return;
+  }
+  const int shift = bytes == 8 ? (sizeof(T) == 2 ? 2 : 1) : sizeof(T) == 2 ? 1 : 0;  // elements: 1 << shift
   const int n = WIDTH >> shift;  // copies a row
 #pragma unroll 4
   for (int e = threadIdx.x; e < rows * n; e += THREADS) {
@@ -185,8 +202,7 @@ __device__ __noinline__ void stage_rows_narrow(T (*dst)[WIDTH], const T* src, lo
     const T* p = src + r * stride + k;
     const int have = (len - k) * (int)sizeof(T);
     if (bytes == 8) copy_async<8>(&dst[r][k], p, min(8, have));
-    else if (bytes == 4) copy_async<4>(&dst[r][k], p, min(4, have));
-    else dst[r][k] = *p;
+    else copy_async<4>(&dst[r][k], p, min(4, have));
   }
 }
 template <typename T, int WIDTH, int ROWS, int THREADS>
