@@ -12,7 +12,7 @@
 // thread then takes RU = 2 rows at once, so that their loads and exchanges overlap;
 // longer ones take a CTA.  Sums are fp32.  HBM-bound: the traffic is the inputs
 // once and the outputs once.  16384 rows of 4096 bf16 with residual: 86 us, 6.2
-// TB/s; backward with ds 89 us, 6.0 TB/s; 524288 rows of 128 to e4m3: 48 us, 4.2
+// TB/s; backward with ds 89 us, 6.0 TB/s; 524288 rows of 128 to e4m3: 50 us, 4.0
 // TB/s (two rows of a thread share too little: issue shows); 3001 rows of 1153 fp32
 // to e4m3, element by element: 13 us, 3.4 TB/s.
 #pragma once
@@ -93,6 +93,37 @@ __device__ __forceinline__ void store_fp8(uint8_t* p, const float (&v)[VEC]) {
     }
     if constexpr (VEC == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+}
+
+// v /= scale, rounded as a division is, so that q is e4m3(y / scale) of the very
+// scale that is stored and a quotient half way between two e4m3 values goes to
+// the even one (one ten-thousandth of the quotients of bf16 rows are: the norm's
+// factor cancels in them).  A quotient q by an approximate reciprocal i becomes
+// q + (y - q scale) i, the remainder exact in a fused multiply-add (P. Markstein,
+// IBM J. Res. Dev. 34, 1990).  An infinite scale gives 0, and NaN for what is
+// infinite itself.
+template <int VEC>
+__device__ __forceinline__ void divide_by(float (&v)[VEC], float scale) {
+  const bool inf = scale == INFINITY;
+  float i = fast_rcp(scale);  // no flush: 1 / scale is between 1.3e-36 and 4.5e12
+  i = inf ? 0.f : fmaf(i, fmaf(-scale, i, 1.f), i);
+  const float d = inf ? 0.f : scale;
+  // the remainder as q scale - y, times -i: so that -0 stays -0
+  if constexpr (VEC % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 q = mul2(make_float2(v[e], v[e + 1]), dup2(i));
+      const float2 r = fma2(fma2(q, dup2(d), make_float2(-v[e], -v[e + 1])), dup2(-i), q);
+      v[e] = r.x;
+      v[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float q = v[e] * i;
+      v[e] = fmaf(fmaf(q, d, -v[e]), -i, q);
+    }
   }
 }
 
@@ -255,15 +286,11 @@ __global__ void __launch_bounds__(threads_of(TPR)) kda_rms_norm_fwd_kernel(const
             for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
           }
           // m / 448, within a unit in the last place; the floor's quotient is exact
-          const bool floored = m <= kScaleFloor;
-          m = max_nan(m, kScaleFloor);
+          const float scale = m <= kScaleFloor ? kScaleFloor / kFp8Max : m * (1.f / kFp8Max);
           if (live && c < nvec && (QUANT >= kGroup ? j % GL == 0 : c == 0))
-            scp[u * a.groups + (QUANT >= kGroup ? i * (TPR / GL) : 0)] =
-                floored ? kScaleFloor / kFp8Max : m * (1.f / kFp8Max);
-          // 448 / m: the reciprocal's argument scaled down, so that a huge m does not flush it to 0
-          const float inv = fast_rcp(m * 0x1p-10f) * (kFp8Max * 0x1p-10f);
+            scp[u * a.groups + (QUANT >= kGroup ? i * (TPR / GL) : 0)] = scale;
           if (live && c < nvec) {
-            scale_by<VEC>(v[u][i], inv);
+            divide_by<VEC>(v[u][i], scale);
             store_fp8<VEC>(reinterpret_cast<uint8_t*>(yp) + u * a.D + i * TPR * VEC, v[u][i]);
           }
         }

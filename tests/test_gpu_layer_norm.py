@@ -214,3 +214,47 @@ def test_many_rows(cuda_device, rows, D, dtype):
     terms = g * sd * r
     # a column's sum in fp32: chains of up to rows / 148 additions, each off by 2^-24 of what it holds
     assert bool(((out["dweight"].to(F64) - terms.sum(0)).abs() <= (2 * K + rows / 148 * 2.0 ** -24) * terms.abs().sum(0)).all())
+
+
+@pytest.mark.parametrize("rows,D,group", [(5000, 128, 128), (4096, 128, 32), (900, 1153, 0), (300, 4096, 128), (700, 2048, 0),
+                                          (3000, 17, 0), (64, 16384, 64)])
+def test_quantised_values_are_the_quotients_rounded_once(cuda_device, rows, D, group):
+    """q is e4m3(y / scale) to the bit: y as the fp32 norm gives it (the same rows in the same threads), scale as
+    returned, the quotient rounded to fp32 and then to e4m3.  Without the rounding of a division, quotients next to a
+    border between two e4m3 values land on the wrong side of it."""
+    x, w, res = _inputs(cuda_device, rows, D, torch.float32, rows + D, True)
+    x, res, w = x.to(torch.bfloat16).float(), res.to(torch.bfloat16).float(), w.to(torch.bfloat16).float()
+    y, _ = kda.rms_norm_fwd(x, w, res)
+    q, scale, _ = kda.rms_norm_quant_fwd(x, w, res, group=group)
+    yg = y.view(rows, -1, group or D)
+    want = (yg / scale[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(rows, D)
+    assert int((q.view(torch.uint8) != want.view(torch.uint8)).sum()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group", [(128, 128), (128, 0), (96, 32), (33, 0), (4096, 64)])
+def test_quotients_half_way_go_to_the_even_value(cuda_device, D, group, dtype):
+    """Rows of +-4 and weights that are whole numbers of at most 8 bits over 64: y = s / 4 * w = +-w, the largest one
+    7 = 448 / 64, the scale 1 / 64 exactly, y / scale whole numbers, many of them half way between two e4m3 values."""
+    dt = DT[dtype]
+    g = torch.Generator(device=cuda_device).manual_seed(D)
+    k = torch.randint(0, 225, (D,), generator=g, device=cuda_device)
+    k[:: group or D] = 224  # every group's largest
+    w = (k.float() / 32).to(dt)
+    x = torch.where(torch.rand(50, D, generator=g, device=cuda_device) < 0.5, -4.0, 4.0).to(dt)
+    q, scale, _ = kda.rms_norm_quant_fwd(x, w, eps=0.0, group=group)
+    assert bool((scale == 1 / 64).all())
+    v = (2 * k.float() * x.float().sign())
+    assert torch.equal(q.view(torch.uint8), v.to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+def test_infinite_scales(cuda_device):
+    """A weight so large that y is infinite: the group's scale is infinite, its finite values 0, the infinite one NaN."""
+    x = torch.ones(3, 128, device=cuda_device)
+    w = torch.ones(128, device=cuda_device)
+    x[1, 5], w[5] = 8.0, 3e38
+    for group in (0, 32):
+        q, scale, _ = kda.rms_norm_quant_fwd(x, w, eps=0.0, group=group)
+        y, _ = kda.rms_norm_fwd(x, w, eps=0.0)
+        assert bool(torch.isinf(y[1, 5])) and bool(torch.isinf(scale[1, 0])) and bool(torch.isfinite(scale[[0, 2]]).all())
+        assert bool(torch.isnan(q[1, 5].float())) and torch.count_nonzero(q[1, :5].float()) == 0
