@@ -225,7 +225,9 @@ __device__ __forceinline__ void stage_rows(T (*dst)[WIDTH], const T* src, long l
 //   of its deltas.  kLocalBwd: also the gradient that a chunk sends to the state
 //   before it, with nothing coming from its right:
 //     sum_t (prod_{s <= t} a_s) C_t dyy_t,  dyy = dy silu(z), up to the first
-//   sequence start in the chunk.
+//   sequence start in the chunk.  The sum is written where that start is met: a
+//   NaN or infinity behind it belongs to another sequence, and times a product
+//   of decays set to zero it would still be one.
 //
 // Inputs arrive by asynchronous copies, two tiles ahead.  kStep tokens inside
 // one sequence run without a branch, so that the exponentials of later tokens
@@ -318,7 +320,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   constexpr int NPB = MODE == kLocalBwd ? NP : 1;
   float2 P[NPB], R[NPB];  // kLocalBwd: product of the decays so far, gradient sent to the left
 #pragma unroll
-  for (int i = 0; i < NPB; ++i) P[i] = dup2(cut ? 0.f : 1.f), R[i] = dup2(0.f);
+  for (int i = 0; i < NPB; ++i) P[i] = dup2(1.f), R[i] = dup2(0.f);
+  auto send_left = [&] {
+    if constexpr (MODE == kLocalBwd)
+      if (active) store_state<NP, LPC * 4>(a.exitg + chunk * a.d * S + crow, R);
+  };
+  if (cut) send_left();
   float sumd = 0.f;  // of the tokens that this lane prepares
 
   // the first of the lane's own tokens of a step, as reduce_scatter deals them
@@ -338,10 +345,10 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
     if (MODE == kForward && a.S_out && active) store_state<NP, LPC * 4>(a.S_out + (long long)n * a.d * S + crow, h);
     n = next_seq(a.q, n, t);
     end = seq_end(a.q, n);
+    if (!cut) send_left();  // what P and R add up from here on is not used
     cut = true;
     if (a.S0) load_state<NP, LPC * 4>(a.S0 + (long long)n * a.d * S + crow, h);
     else zero_state<NP>(h);
-    if (MODE == kLocalBwd) zero_state<NPB>(P);
   };
   // one token of the lane's states -> its part of C . h.  gv: dy silu(z) (kLocalBwd); last: with dS
   auto token = [&](float2 dd, float2 uu, float gv, const float* tb, const float* tc, bool last) -> float {
@@ -490,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_selective_scan_kernel(const A
   } else {
 #pragma unroll
     for (int o = LPC / 2; o > 0; o >>= 1) sumd += __shfl_xor_sync(0xffffffffu, sumd, o);
+    if (!cut) send_left();
     if (active) {
       store_state<NP, LPC * 4>(a.entry + chunk * a.d * S + crow, h);
-      if constexpr (MODE == kLocalBwd) store_state<NP, LPC * 4>(a.exitg + chunk * a.d * S + crow, R);
       if (sl == 0) a.sumd[chunk * a.d + c] = cut ? -1.f : sumd;
     }
   }

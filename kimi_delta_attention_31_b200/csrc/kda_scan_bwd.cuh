@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
       auto local_sweep = [&](auto with_edges) {
         constexpr bool kEdges = decltype(with_edges)::value;
         float2 h0 = dup2(0.f), h1 = dup2(0.f), P0 = dup2(1.f), P1 = dup2(1.f), r0 = dup2(0.f), r1 = dup2(0.f);
+        bool open = true;  // no sequence has started among the warp's tokens yet: what comes after a start is sent to nobody
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
           const int t = tw + k;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
               const float4 v = *reinterpret_cast<const float4*>(S0g + (long long)s.first[t] * a.d * S + crow);
               h0 = lo2(v), h1 = hi2(v);
             }
-            P0 = P1 = dup2(0.f);
+            open = false;
           }
           h0 = fma2(da[k][0], h0, mul2(hi2(du), lo2(b4)));
           h1 = fma2(da[k][1], h1, mul2(hi2(du), hi2(b4)));
@@ -231,8 +232,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) kda_selective_scan_bwd_kernel(
             g0 = add2(g0, lo2(v));
             g1 = add2(g1, hi2(v));
           }
-          r0 = fma2(P0, g0, r0);
-          r1 = fma2(P1, g1, r1);
+          if (!kEdges || open) {
+            r0 = fma2(P0, g0, r0);
+            r1 = fma2(P1, g1, r1);
+          }
         }
         *reinterpret_cast<float4*>(&s.P[warp][lane * 4]) = make_float4(P0.x, P0.y, P1.x, P1.y);
         *reinterpret_cast<float4*>(&s.H[warp][lane * 4]) = make_float4(h0.x, h0.y, h1.x, h1.y);

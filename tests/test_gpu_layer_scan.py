@@ -305,3 +305,39 @@ def test_many_short_sequences_and_more_than_a_grid_dimension_of_steps(cuda_devic
     sub = {k: (t[at] if k in ("x", "dt", "z", "B", "C") else t) for k, t in w.items()}
     sub["S0"] = keep[at]
     _check_fwd(sub, [1] * len(at), y[at], w["S0"][at])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["dy", "z", "C", "B", "dt", "x", "dS", "S0"])
+@pytest.mark.parametrize("lens,d,S,groups", [((200, 70, 90, 150), 37, 16, 1), ((128, 128, 128), 33, 16, 1),
+                                             ((300, 300), 36, 64, 2), ((64, 0, 1, 64, 191, 3), 20, 8, 2)])
+def test_non_finite_values_stay_with_their_sequence(cuda_device, lens, d, S, groups, name, value):
+    """A NaN or infinity that enters one sequence, forward or backward: every output of the others is what it was, to
+    the bit.  Starts inside a tile of tokens and on its border, in the middle of eight tokens and on theirs, sequences of
+    several tiles before it, packed and in rows."""
+    packed = len(set(lens)) > 1
+    v = _inputs(cuda_device, lens, d, S, groups, torch.float32, 51, packed)
+    dy, dS = torch.randn_like(v["x"]), torch.randn(len(lens), d, S, device=cuda_device)
+    ry, rS = _fwd(v)
+    ref = _bwd(v, dy, dS)
+    at, total = R.bounds(lens), sum(lens)
+    rows = lambda t: t.reshape(total, *t.shape[2:])
+    for n in range(len(lens)):
+        for back in sorted({0, lens[n] // 2, max(lens[n] - 1, 0)}):
+            if name not in ("dS", "S0") and back >= lens[n]:
+                continue
+            w, gy, gS = {k: None if t is None else t.clone() for k, t in v.items()}, dy.clone(), dS.clone()
+            if name in ("dS", "S0"):
+                (gS if name == "dS" else w["S0"])[n, d // 2, S // 2] = value
+            else:
+                t = rows(gy if name == "dy" else w[name])[at[n] + back]
+                t.view(-1)[t.numel() // 2] = value
+            y, So = _fwd(w)
+            out = _bwd(w, gy, gS)
+            others = torch.ones(total, dtype=torch.bool, device=cuda_device)
+            others[at[n]:at[n + 1]] = False
+            seqs = [i for i in range(len(lens)) if i != n]
+            for what, a, b in [("y", y, ry)] + [(k, out[k], ref[k]) for k in ("dx", "ddt", "dz", "dB", "dC")]:
+                assert torch.equal(rows(a)[others], rows(b)[others]), (what, n, back)
+            assert torch.equal(So[seqs], rS[seqs]) and torch.equal(out["dS0"][seqs], ref["dS0"][seqs]), (n, back)
+    assert kda.device_error() == 0
