@@ -422,7 +422,9 @@ __global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / thread
     }
     row_reduce<TPR, false>(sums, s_red[buf]);
     const float r = rsqrtf(sums[0] * inv_d + a.eps);
-    const float k = r * r * r * (sums[1] * inv_d);
+    // r^3 mean(w dy s), a factor r at a time: r^3 alone leaves fp32's range from rows of 1e13 on, and with eps = 0 below
+    // 1e-13
+    const float k = sums[1] * inv_d * r * r * r;
     if (live) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {

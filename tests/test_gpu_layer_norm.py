@@ -258,3 +258,21 @@ def test_infinite_scales(cuda_device):
         y, _ = kda.rms_norm_fwd(x, w, eps=0.0)
         assert bool(torch.isinf(y[1, 5])) and bool(torch.isinf(scale[1, 0])) and bool(torch.isfinite(scale[[0, 2]]).all())
         assert bool(torch.isnan(q[1, 5].float())) and torch.count_nonzero(q[1, :5].float()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,eps", [(1e15, 1e-6), (1e17, 1e-6), (1e-13, 0.0), (1e-17, 0.0)])
+@pytest.mark.parametrize("rows,D", [(5, 128), (3, 1001), (4, 4096), (2, 16384)])
+def test_backward_of_rows_far_from_one(cuda_device, rows, D, scale, eps, dtype):
+    """dx is 1 / scale of the unit rows' while mean(s^2) is inside fp32's range (1e-34 to 1e34 here)."""
+    dt = DT[dtype]
+    s, w, dy = _inputs(cuda_device, rows, D, dt, 7 * rows + D, True)
+    s = (s.float() * scale).to(dt)
+    out = kda.rms_norm_bwd(dy, s, w, eps=eps)
+    c = lambda t: t.cpu().to(F64)
+    g = R.grads(lambda x, weight: (R.norm(x, weight, eps=eps)[0],), dict(x=c(s), weight=c(w)), [c(dy)])
+    r = 1 / (c(s).square().mean(-1, keepdim=True) + eps).sqrt()
+    size = (r * c(w) * c(dy)).abs() + c(s).abs() * r ** 3 * (c(w) * c(dy) * c(s)).abs().mean(-1, keepdim=True)
+    # mean(s^2) of 1e-34 is 1e4 times fp32's smallest normal value: the bounds of unit rows hold
+    within(out["dx"], g["x"], U[dt] * g["x"].abs() + 4 * K * size, "dx")
+    within(out["dweight"], g["weight"], 2 * K * (c(dy) * c(s) * r).abs().sum(0), "dweight")
