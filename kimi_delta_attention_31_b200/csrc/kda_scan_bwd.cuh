@@ -503,7 +503,7 @@ cudaError_t launch_bwd(Args a, BwdOut o, float* dA, float* dB, float* dC, float*
   a.chunks = p.tiles;
   cudaError_t e;
   const long long row = (long long)a.d * S;
-  if (o.dS0 && (a.q.cu || tokens == 0)) {
+  if (o.dS0 && a.q.num > 0 && (a.q.cu || tokens == 0)) {
     const int grid = a.q.num < 1024 ? a.q.num : 1024;
     kda_scan_empty_bwd_kernel<<<grid, 256, 0, st>>>(a.q, a.dS, o.dS0, row);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

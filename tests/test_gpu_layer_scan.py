@@ -341,3 +341,24 @@ def test_non_finite_values_stay_with_their_sequence(cuda_device, lens, d, S, gro
                 assert torch.equal(rows(a)[others], rows(b)[others]), (what, n, back)
             assert torch.equal(So[seqs], rS[seqs]) and torch.equal(out["dS0"][seqs], ref["dS0"][seqs]), (n, back)
     assert kda.device_error() == 0
+
+
+def test_backward_of_an_empty_batch_through_the_c_abi(cuda_device):
+    """No rows, every output given: the sums over tokens are zeros, as the convolution's and the norm's are."""
+    d, S = 24, 16
+    f = lambda *s: torch.full(s, 7.0, device=cuda_device)
+    p = lambda t: t.data_ptr()
+    x, B, A, v, kept = f(8, d), f(8, S), f(d, S), f(d), f(2, d, S)
+    out = dict(dx=f(8, d), ddt=f(8, d), dA=f(d, S), dB=f(8, S), dC=f(8, S), dD=f(d), dz=f(8, d), db=f(d), dS0=f(2, d, S))
+    for nb, T in ((0, 4), (0, 0)):
+        for t in out.values():
+            t.fill_(7.0)
+        st = kda.load_library().kda_selective_scan_bwd(
+            p(x), d, p(x), d, p(A), p(B), S, p(B), S, p(v), p(x), d, p(v), p(kept), p(x), p(kept), p(out["dx"]),
+            p(out["ddt"]), p(out["dA"]), p(out["dB"]), p(out["dC"]), p(out["dD"]), p(out["dz"]), p(out["db"]),
+            p(out["dS0"]), None, 0, nb, T, d, S, 1, kda.KDA_F32, None, 0, torch.cuda.current_stream().cuda_stream)
+        assert st == 0, kda.last_error()
+        for name in ("dA", "dD", "db"):
+            assert torch.count_nonzero(out[name]) == 0, name
+        for name in ("dx", "ddt", "dB", "dC", "dz", "dS0"):
+            assert bool((out[name] == 7.0).all()), name
