@@ -746,7 +746,10 @@ def _on(dev):
     return _SAME_DEVICE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _raw_stream(dev):
+    """Handle of the current stream of device `dev` (looked up in the call: a
+    torch built without CUDA has no such name, and imports this package)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _dense_like(x, dtype=None):

@@ -2,6 +2,9 @@
 rejects bad arguments before any launch, and the binding rejects wrong types,
 shapes and layouts before it reaches the C ABI."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -200,3 +203,20 @@ def test_binding_refuses_types_shapes_and_layouts():
         kda.selective_scan_bwd(x, x, A, B, B, x.float())
     with pytest.raises(TypeError):
         kda.selective_scan_step(x[0], x[0], A, B[0], B[0], torch.zeros(8, 16, 8, dtype=bf))
+
+
+def test_import_on_a_torch_without_cuda():
+    """The package imports, and refuses host tensors, where torch lacks the names of its CUDA build."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, n)\n"
+            "import kimi_delta_attention_31_b200 as kda\n"
+            "try:\n"
+            "    kda.rms_norm_fwd(torch.zeros(2, 16), torch.zeros(16))\n"
+            "except ValueError as e:\n"
+            "    assert 'CUDA' in str(e)\n"
+            "else:\n"
+            "    raise SystemExit(1)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert done.returncode == 0, done.stderr
