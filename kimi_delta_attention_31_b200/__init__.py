@@ -734,6 +734,12 @@ def _act_code(name, t):
     return code
 
 
+def _check_sizes(name, shape):
+    """The C ABI takes sizes as 32-bit integers, to which ctypes cuts larger ones without a word."""
+    if max(shape) >= 1 << 31:
+        raise ValueError(f"{name}: a dimension of 2^31 or more ({tuple(shape)})")
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -773,6 +779,7 @@ def _norm_dim(x):
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"x must be [..., D], got {tuple(x.shape)}")
     D = x.shape[-1]
+    _check_sizes("x", (D,))  # rows are 64 bits wide
     return D, x.numel() // D
 
 
@@ -853,6 +860,7 @@ def _sequences(x, cu_seqlens):
         raise TypeError("cu_seqlens must be a 1-D int32 tensor of num_seqs + 1 entries")
     if B != 1:
         raise ValueError("packed sequences (cu_seqlens) need B == 1")
+    _check_sizes("cu_seqlens", cu_seqlens.shape)
     n = cu_seqlens.numel() - 1
     return B, T, n, n
 
@@ -860,6 +868,7 @@ def _sequences(x, cu_seqlens):
 def _conv_dim(x, weight, dims):
     if x.dim() != dims:
         raise ValueError(f"x must be {'[B,T,D]' if dims == 3 else '[N,D]'}, got {tuple(x.shape)}")
+    _check_sizes("x", x.shape)
     D = x.shape[-1]
     if weight.dim() != 2 or weight.shape[0] != D or not 2 <= weight.shape[1] <= 4:
         raise ValueError(f"weight must be [D={D}, W] with W 2, 3 or 4, got {tuple(weight.shape)}")
@@ -956,6 +965,8 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dims, more):
     d = shape[-1]
     if A.dim() != 2 or A.shape[0] != d:
         raise ValueError(f"A must be [d={d}, S], got {tuple(A.shape)}")
+    _check_sizes("x", shape)
+    _check_sizes("A", A.shape)
     if B.dim() != dims + 1:
         raise ValueError(f"B must be [..., groups, S], got {tuple(B.shape)}")
     S, groups = A.shape[1], B.shape[-2]

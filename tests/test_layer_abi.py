@@ -220,3 +220,25 @@ def test_import_on_a_torch_without_cuda():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert done.returncode == 0, done.stderr
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """A size that the C ABI's 32-bit integers would be cut to a small one (tensors without memory: nothing is read)."""
+    n = (1 << 32) + 16
+    e = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="meta")
+    calls = [lambda: kda.rms_norm_fwd(e(2, n), e(n)), lambda: kda.rms_norm_quant_fwd(e(2, n), e(n)),
+             lambda: kda.rms_norm_bwd(e(2, n), e(2, n), e(n)),
+             lambda: kda.short_conv_fwd(e(1, n, 1), e(1, 4)), lambda: kda.short_conv_fwd(e(n, 1, 1), e(1, 4)),
+             lambda: kda.short_conv_bwd(e(1, 1, n), e(n, 4), e(1, 1, n)),
+             lambda: kda.short_conv_step(e(n, 1), e(1, 4), e(n, 3, 1)),
+             lambda: kda.short_conv_fwd(e(1, 1, 1), e(1, 4), cu_seqlens=e(n, dtype=torch.int32))]
+    f32 = torch.float32
+    for B, T, d, S in ((1, n, 1, 8), (n, 1, 1, 8), (1, 1, n, 8), (1, 1, 1, n)):
+        x, A, b = e(B, T, d), e(d, S, dtype=f32), e(B, T, 1, S)
+        calls.append(lambda x=x, A=A, b=b: kda.selective_scan_fwd(x, x, A, b, b))
+        calls.append(lambda x=x, A=A, b=b: kda.selective_scan_bwd(x, x, A, b, b, x))
+    x, b = e(n, 1), e(n, 1, 8)
+    calls.append(lambda: kda.selective_scan_step(x, x, e(1, 8, dtype=f32), b, b, e(n, 1, 8, dtype=f32)))
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
