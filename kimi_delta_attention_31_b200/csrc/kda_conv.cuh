@@ -465,9 +465,15 @@ inline long long fwd_run(long long tokens, int ncol) {
 }
 // Backward runs: every run writes a line of partial sums, so no more of them
 // than run at once (four CTAs an SM; six: 123.6 us against 117.0 for 16384
-// tokens of 4096 channels), none under 16 tokens.
+// tokens of 4096 channels), none under 16 tokens.  The runs of a column block
+// are counted first, rounded down: a few CTAs in a second wave would each walk
+// a whole run on a card that is otherwise done (12288 channels, 24 runs of a
+// column block against 25: 65536 tokens 1200 and 1404 us, 16384 tokens 315 and
+// 318; 16384 channels, 18 against 19: 16384 tokens 431 and 420).
+constexpr long long kBwdWave = 148 * 4;
 inline long long bwd_run(long long tokens, int ncol) {
-  long long L = (tokens * ncol + 148 * 4 - 1) / (148 * 4);
+  const long long runs = ncol < kBwdWave ? kBwdWave / ncol : 1;
+  long long L = (tokens + runs - 1) / runs;
   L = L < 16 ? 16 : L;
   return (L + kGroup - 1) / kGroup * kGroup;
 }

@@ -242,3 +242,12 @@ def test_binding_refuses_sizes_past_32_bits():
     for i, call in enumerate(calls):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+@pytest.mark.parametrize("D", [512, 1000, 4096, 7168, 8192, 10240, 12288, 14336, 16384, 40000])
+def test_conv_backward_runs_fit_one_wave(D):
+    """A line of partial sums per run, as many runs of 512 channels as 148 SMs take at four CTAs each, or fewer."""
+    size = kda.load_library().kda_short_conv_bwd_workspace_size
+    for tokens in (1, 15, 600, 8192, 16384, 32769, 65536, 1 << 20):
+        lines = size(1, tokens, D, 4) // (D * 5 * 4)
+        assert 1 <= lines and lines * -(-D // 512) <= 148 * 4, (tokens, lines)
