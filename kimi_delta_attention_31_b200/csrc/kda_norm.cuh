@@ -480,6 +480,9 @@ __global__ void __launch_bounds__(threads_of(TPR), NV * VEC <= 16 ? 512 / thread
 // one vector against two: 31.6 and 27.5 us for 8192 e4m3 rows; four: no better);
 // rows read element by element take one warp group and up to 16 elements a
 // thread (60000 rows of 500: 61 us, with 512 threads and one element 147 us).
+// There, elements past the row's end cost as much as others (8 M bf16 elements in
+// rows of 301: 3 a thread 20.6 us, 4 22.6, 5 24.7, 6 26.8; in rows of 1001: 8 15.5,
+// 10 16.5, 12 20.6, 16 26.7), so no step from 3 on is more than a third.
 struct RowShape {
   int tpr, nv;
 };
@@ -487,7 +490,7 @@ inline RowShape row_shape(int vecs, int vec) {
   for (int tpr = 8; tpr <= 32; tpr *= 2)
     if (vecs <= tpr) return {tpr, 1};
   if (vec == 1) {
-    for (int nv : {1, 2, 5, 10, 16})
+    for (int nv : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16})
       if (vecs <= 128 * nv) return {128, nv};
     for (int nv : {8, 16})
       if (vecs <= 512 * nv) return {512, nv};
@@ -526,8 +529,8 @@ inline RowShape row_shape_bwd(int vecs, int vec) {
 #define KDA_NORM_FWD_WIDE(CASE) \
   KDA_NORM_SMALL(CASE) CASE(64, 1) CASE(128, 1) CASE(128, 2) CASE(256, 2) CASE(512, 2) KDA_NORM_LONG(CASE)
 #define KDA_NORM_FWD_SCALAR(CASE)                                                                                  \
-  KDA_NORM_SMALL(CASE) CASE(128, 1) CASE(128, 2) CASE(128, 5) CASE(128, 10) CASE(128, 16) CASE(512, 8) CASE(512, 16) \
-  CASE(512, 32)
+  KDA_NORM_SMALL(CASE) CASE(128, 1) CASE(128, 2) CASE(128, 3) CASE(128, 4) CASE(128, 5) CASE(128, 6) CASE(128, 8)    \
+  CASE(128, 10) CASE(128, 12) CASE(128, 16) CASE(512, 8) CASE(512, 16) CASE(512, 32)
 #define KDA_NORM_BWD_WIDE(CASE) \
   KDA_NORM_SMALL(CASE) CASE(32, 2) CASE(64, 2) CASE(128, 2) CASE(256, 2) CASE(512, 2) KDA_NORM_LONG(CASE)
 #define KDA_NORM_BWD_SCALAR(CASE)                                                                                   \

@@ -276,3 +276,18 @@ def test_backward_of_rows_far_from_one(cuda_device, rows, D, scale, eps, dtype):
     # mean(s^2) of 1e-34 is 1e4 times fp32's smallest normal value: the bounds of unit rows hold
     within(out["dx"], g["x"], U[dt] * g["x"].abs() + 4 * K * size, "dx")
     within(out["dweight"], g["weight"], 2 * K * (c(dy) * c(s) * r).abs().sum(0), "dweight")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [33, 127, 129, 257, 385, 511, 513, 641, 769, 1023, 1025, 1281, 1535, 1537, 2047, 2049, 4097, 8193])
+def test_rows_at_odd_places_of_every_length(cuda_device, D, dtype):
+    """Rows read element by element: just below and above the lengths at which a thread takes another number of them."""
+    dt = DT[dtype]
+    x, w, res = _inputs(cuda_device, 5, D, dt, D, True)
+    y, s = kda.rms_norm_fwd(x, w, res)
+    q, scale, s2 = kda.rms_norm_quant_fwd(x, w, res)
+    ry, rs = _ref(x, w, res)
+    within(y, ry, (U[dt] + K) * ry.abs(), "y")
+    within(s, rs, (U[dt] * (1 + 2.0 ** -20) + 2.0 ** -24) * rs.abs(), "s")
+    assert torch.equal(s, s2)
+    _check_quant(q, scale, ry, 0)
