@@ -435,9 +435,9 @@ kda_status_t kda_short_conv_bwd(const void* x, long long x_stride, const void* w
  *   S0 : [N, d, S] fp32 or NULL (zeros);  S_out : [N, d, S] fp32 or NULL, not S0
  *   S in {8, 16, 32, 64}; groups divides d.  A, S0, S_out and the workspace
  *       are 16-byte aligned.
- * Batches with few channels and packed sequences are cut into chunks of the
- * token axis that run in parallel (up to rounding the result is the same); the
- * workspace holds one state per chunk.
+ * Calls with few channels (counted over a batch's rows; packed sequences are one
+ * row) are cut into chunks of the token axis that run in parallel (up to rounding
+ * the result is the same); the workspace holds one state per chunk.
  */
 size_t kda_selective_scan_fwd_workspace_size(int B, int T, int d, int S, int groups, int num_seqs);
 kda_status_t kda_selective_scan_fwd(const void* x, long long x_stride, const void* dt, long long dt_stride,

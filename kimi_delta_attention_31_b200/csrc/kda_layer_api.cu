@@ -388,7 +388,7 @@ extern "C" {
 
 size_t kda_selective_scan_fwd_workspace_size(int B, int T, int d, int S, int groups, int num_seqs) {
   if (B < 0 || T < 0 || num_seqs < 0 || d < 1 || groups < 1 || d % groups || !kda::scan::supported_state(S)) return 0;
-  const kda::scan::FwdPlan p = kda::scan::fwd_plan(B, T, num_seqs, d, groups, S);
+  const kda::scan::FwdPlan p = kda::scan::fwd_plan(B, T, d, groups, S);
   if (!p.split) return 0;
   return kda::scan::round256(kda::scan::carry_floats(p.chunks, d, S) * 4) + (size_t)p.chunks * d * 4;
 }
@@ -415,7 +415,7 @@ kda_status_t kda_selective_scan_fwd(const void* x, long long x_stride, const voi
   if (kda_status_t st = check_workspace(fn, workspace, workspace_bytes,
                                         kda_selective_scan_fwd_workspace_size(B, T, d, S, groups, num_seqs)))
     return st;
-  const kda::scan::FwdPlan p = kda::scan::fwd_plan(B, T, num_seqs, d, groups, S);
+  const kda::scan::FwdPlan p = kda::scan::fwd_plan(B, T, d, groups, S);
   a.L = p.L, a.chunks = p.chunks;
   a.ncb = kda::scan::channel_blocks(d, groups, S);
   a.blocks_per_group = a.ncb / groups;

@@ -18,9 +18,9 @@
 // a quarter of the exponentials by polynomial on the FMA pipe (1152, against 1008
 // then).
 //
-// When a batch has too few channels to fill the card, or sequences are packed
-// (their lengths are on the device only), the token axis is cut into chunks
-// wherever they fall: the kernel's kLocal form runs every chunk from a zero state,
+// When a call has too few channels to fill the card (packed sequences, whose
+// lengths are on the device only, count as one row), the token axis is cut into
+// chunks wherever they fall: the kernel's kLocal form runs every chunk from a zero state,
 // kda_scan_carry_kernel chains the chunks (h is linear in the state that enters:
 // a whole chunk multiplies it by exp(A sum delta)), and the scan then runs each
 // chunk from its entry state.  A chunk in which a sequence starts passes
@@ -639,12 +639,17 @@ inline int channel_blocks(int d, int groups, int S) {
   return groups * ((d / groups + ch - 1) / ch);
 }
 
-// Chunks of the forward.  A split costs the exponentials a second time, a batch
+// Chunks of the forward.  A split costs the exponentials a second time, a call
 // without one leaves SMs idle: 4096 tokens of 1024 channels (64 warps a row), split
 // and unsplit: 4 rows 228 and 461 us, 8 rows 409 and 455, 12 rows 588 and 586, 16
-// rows 760 and 585.  So a batch with a warp or more for every SM sub-partition runs
-// unsplit; others, and packed sequences, have the token axis cut so that about 16
-// warps an SM run at once, into chunks of 64 tokens at least.
+// rows 760 and 585.  Packed sequences, whose lengths are on the device only, are
+// one row here: unsplit, a CTA walks all their tokens (4 packed prompts of 2048
+// tokens, 16 states, cut and in one walk: 4096 channels, 256 warps: 1475 and 3307
+// us for 8 of 4096; 8192 channels 841 and 840; 12288 1113 and 1081; 16384 1651 and
+// 1081; uneven lengths the same).  So a call with a warp or more for every SM
+// sub-partition runs unsplit; others have the token axis cut so that about 16
+// warps an SM run at once, into chunks of 64 tokens at least.  A batch's rows of
+// the same sizes run side by side in half to two thirds of the packed time.
 struct FwdPlan {
   bool split;
   long long L, chunks;
@@ -662,12 +667,11 @@ inline void set_copies(Args& a, int S, int esize) {
                       {a.xs, a.dts, a.z ? a.zs : 0, a.dy ? a.d : 0, a.cpg == a.d ? 0 : a.cpg}, esize);
   a.copy_bc = copy_width({a.B, a.C}, {a.bs, a.cs, S}, esize);
 }
-inline FwdPlan fwd_plan(long long B, long long T, int num_seqs, int d, int groups, int S) {
+inline FwdPlan fwd_plan(long long B, long long T, int d, int groups, int S) {
   const long long tokens = B * T;
   const long long warps = (long long)channel_blocks(d, groups, S) * (kThreads / 32);
-  const bool packed = num_seqs > 1;
-  if (!packed && (B * warps >= 148 * 4 || T < 128)) return {false, T > 0 ? T : 1, B};
-  if (tokens < 128) return {false, tokens > 0 ? tokens : 1, 1};
+  // rows that run side by side, and their tokens: B of T, or all packed sequences as one (then B == 1)
+  if (B * warps >= 148 * 4 || T < 128) return {false, T > 0 ? T : 1, B};
   long long chunks = 148 * 16 / warps;
   if (chunks < 1) chunks = 1;
   long long L = (tokens + chunks - 1) / chunks;

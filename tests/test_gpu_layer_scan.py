@@ -362,3 +362,16 @@ def test_backward_of_an_empty_batch_through_the_c_abi(cuda_device):
             assert torch.count_nonzero(out[name]) == 0, name
         for name in ("dx", "ddt", "dB", "dC", "dz", "dS0"):
             assert bool((out[name] == 7.0).all()), name
+
+
+@pytest.mark.parametrize("dtype,d,S", [("f32", 4800, 64), ("bf16", 9500, 16)])
+def test_packed_sequences_wide_enough_for_one_walk(cuda_device, dtype, d, S):
+    """Channels that fill the card: packed sequences run unsplit too, as a batch does, and take no workspace."""
+    lens = (40, 0, 90, 1, 7)
+    size = kda.load_library().kda_selective_scan_fwd_workspace_size
+    assert size(1, sum(lens), d, S, 1, len(lens)) == 0 and size(1, sum(lens), d // 2, S, 1, len(lens)) > 0
+    assert size(16, 128, d // 16, S, 1, 0) == 0  # as many channels in rows
+    v = _inputs(cuda_device, lens, d, S, 1, DT[dtype], 61, True)
+    y, So = _fwd(v)
+    assert kda.device_error() == 0
+    _check_fwd(v, lens, y, So)
