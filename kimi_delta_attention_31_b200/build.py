@@ -16,7 +16,9 @@ UNITS = [os.path.join(CSRC, "kda_api.cu"), os.path.join(CSRC, "kda_layer_api.cu"
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC",
+    # without unique symbols: two copies of the library in one process would share
+    # which kernels have been set up, and the second copy's never would be
+    "-Xcompiler", "-fPIC,-fno-gnu-unique",
     "-Xptxas", "-warn-spills",
     "--expt-relaxed-constexpr",
 ]

@@ -251,3 +251,12 @@ def test_conv_backward_runs_fit_one_wave(D):
     for tokens in (1, 15, 600, 8192, 16384, 32769, 65536, 1 << 20):
         lines = size(1, tokens, D, 4) // (D * 5 * 4)
         assert 1 <= lines and lines * -(-D // 512) <= 148 * 4, (tokens, lines)
+
+
+def test_no_symbol_is_shared_between_loaded_copies():
+    """Static variables of inline functions (which kernels have been set up on a device) belong to their copy of the
+    library: as unique symbols the first copy in a process would own them for all."""
+    kda.load_library()
+    out = subprocess.run(["nm", "-D", "--defined-only", kda.lib_path()], capture_output=True, text=True, check=True).stdout
+    kinds = [line.split()[1] for line in out.splitlines()]
+    assert "T" in kinds and "u" not in kinds
