@@ -11,10 +11,10 @@
 // neighbouring vectors.  Rows of up to 32 vectors take part of a warp, and a
 // thread then takes RU = 2 rows at once, so that their loads and exchanges overlap;
 // longer ones take a CTA.  Sums are fp32.  HBM-bound: the traffic is the inputs
-// once and the outputs once.  16384 rows of 4096 bf16 with residual: 86 us, 6.2
-// TB/s; backward with ds 89 us, 6.0 TB/s; 524288 rows of 128 to e4m3: 50 us, 4.0
+// once and the outputs once.  16384 rows of 4096 bf16 with residual: 84 us, 6.4
+// TB/s; backward with ds 89 us, 6.0 TB/s; 524288 rows of 128 to e4m3: 51 us, 4.0
 // TB/s (two rows of a thread share too little: issue shows); 3001 rows of 1153 fp32
-// to e4m3, element by element: 13 us, 3.4 TB/s.
+// to e4m3, element by element: 11 us, 4.1 TB/s.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -538,8 +538,9 @@ inline RowShape row_shape_bwd(int vecs, int vec) {
   CASE(512, 32)
 
 // Turns of the forward's small rows: the set-up of a thread is worth several
-// rows, as long as every SM has 8 CTAs (524288 rows of 128 to e4m3: 48.2 us; at 8
-// turns and 32 CTAs 49.2).
+// rows, as long as every SM has 8 CTAs (e4m3 output, at most 8, 16 and 32 turns:
+// 524288 rows of 128 bf16 51.2, 51.7 and 55.8 us, 300000 rows of 100 fp32 47.8, 46.1
+// and 51.9; 4 or 16 CTAs: no difference).
 inline int fwd_turns(long long rows, int rows_a_turn) {
   const long long t = rows / ((long long)rows_a_turn * 148 * 8);
   return (int)(t < 1 ? 1 : t > 16 ? 16 : t);

@@ -21,11 +21,15 @@
 // (summing them for every token took a fifth of the instructions).  Sums over
 // tokens or channel blocks leave as lines that a second kernel adds in order.
 //
-// 4 x 2048 tokens of 4096 channels, 16 states: 1503 us, of which this kernel 1.2
-// ms, the local scan 250 us, carry and sums 45.  Bound by issue and shared-memory
-// reads at one CTA of 8 warps an SM (255 registers: the decays, entering states and
-// channel sums of 8 tokens by 4 states a lane).  More, smaller warps' shares were
-// slower: 6 tokens and 12 warps 8%, 4 tokens and 16 warps 9%.
+// 4 x 2048 tokens of 4096 channels, 16 states: 1515 us, of which this kernel 1.24
+// ms, the local scan 232 us, carry and sums 48.  Bound by latency: at 255 registers
+// (the decays, entering states and channel sums of 8 tokens by 4 states a lane) one
+// CTA of 8 warps fits an SM, an eighth of its warps, which wait for their own
+// results and at two barriers for every 32 / (S / 4) channels; no pipe is full
+// (issue 39%, L1 and shared memory 46%, exponential unit 13%, DRAM 4%).  Smaller
+// shares in one larger CTA were slower, its chain being longer: 6 tokens and 12
+// warps 8%, 4 tokens and 16 warps 9%.  Not tried: taking the decays again in the
+// reverse sweep, which would make room for a second, independent CTA.
 #pragma once
 #include <type_traits>
 
