@@ -808,8 +808,9 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=None, s=None):
 
 def rms_norm_quant_fwd(x, weight, residual=None, eps=1e-6, group=0, s=None):
     """rms_norm_fwd with an e4m3 output: scale = max(amax |y|, 1e-10) / 448 over
-    each group of `group` columns (32, 64 or 128; 0: the whole row), q = y /
-    scale.  Returns (q [..., D] float8_e4m3fn, scale [..., D / group] fp32, s)."""
+    each group of `group` columns (32, 64 or 128, which need rows and tensors at
+    16-byte places; 0: the whole row), q = y / scale rounded to nearest even.
+    Returns (q [..., D] float8_e4m3fn, scale [..., D / group] fp32, s)."""
     lib = _lib or load_library()
     code, wcode, dev, shape, dtype = _act_code("x", x), _act_code("weight", weight), x.get_device(), x.shape, x.dtype
     D, rows = _norm_dim(x)
